@@ -399,6 +399,101 @@ int32_t gemm_variant_count(void);
  * index or NULL out. */
 int gemm_variant_get(int32_t i, gemm_variant_info *out);
 
+/* ---- products whose rows choose their matrix -------------------------------
+ *
+ * A mixture-of-experts layer multiplies each row by the matrices of the
+ * experts its router chose; a server of many adapters multiplies each row by
+ * the two small matrices of its request's adapter.  Rows are first sorted by
+ * group (gemm_route, gemm_gather_rows), multiplied group by group
+ * (gemm_grouped_run) and added up again (gemm_combine_rows).  Group sizes are
+ * known on the GPU only, so none of these calls takes them from the host, and
+ * none waits for the GPU: row counts change from call to call, and there is no
+ * plan to make.  All of them can be captured into a HIP graph.
+ *
+ * An id outside [0, groups) (-1 by convention) chooses nothing: its entry is
+ * dropped.  Index buffers are read on the GPU and may hold anything: a
+ * position or an offset out of range never makes a kernel read or write
+ * outside the buffers described here, it only gives rows nobody asked for.
+ *
+ * All calls are asynchronous on stream (a hipStream_t; NULL = the default
+ * stream) and allocate nothing; every pointer is a device pointer, aligned to
+ * its element, and owned by the caller.  Each returns 0, -1 (invalid
+ * argument), -2 (workspace missing) or -3 (HIP launch error), with a message
+ * in gemm_last_error(). */
+
+/* Sort entries by group.  Entry i = t * choices + j is choice j of token t,
+ * ids its group (int32 or int64: id_bytes 4 or 8), tokens x choices, dense.
+ * Writes, stably (entries of a group keep their order):
+ *   offsets[0 .. groups]   group g owns sorted rows offsets[g] .. offsets[g + 1] - 1,
+ *                          and offsets[groups] is the number of entries kept;
+ *   order[row]             the entry at a sorted row, -1 past the kept ones;
+ *   position[i]            the sorted row of entry i, -1 if it is dropped.
+ * tokens * choices < 2^31, 1 <= groups <= 16382.  The workspace (4-byte
+ * aligned) needs no clearing. */
+int gemm_route(const void *ids, int32_t id_bytes, int64_t tokens, int32_t choices, int32_t groups,
+               int32_t *offsets, int32_t *order, int32_t *position, void *workspace, void *stream);
+
+/* Bytes of workspace gemm_route needs (0: none). */
+size_t gemm_route_workspace_size(int64_t tokens, int32_t choices, int32_t groups);
+
+/* xs[position[t][j]] = x[t]: the tokens' rows (tokens x cols, dense) in sorted
+ * order.  kept points to the number of rows kept (offsets + groups of
+ * gemm_route); rows past it are zeroed, so xs (tokens * choices x cols) is
+ * written whole.  fp32, fp16 or bf16 rows; cols < 2^22. */
+int gemm_gather_rows(const void *x, const int32_t *position, const int32_t *kept, void *xs,
+                     int64_t tokens, int32_t choices, int64_t cols, gemm_dtype dtype, void *stream);
+
+/* y[t] = sum over j of weights[t][j] * ys[position[t][j]], summed in fp32 in
+ * the order of j and rounded once; a dropped choice's row is not read.
+ * weights NULL: the plain sum (the gradient of gemm_gather_rows). */
+int gemm_combine_rows(const void *ys, const int32_t *position, const float *weights, void *y,
+                      int64_t tokens, int32_t choices, int64_t cols, gemm_dtype dtype,
+                      void *stream);
+
+/* The gradients of gemm_combine_rows (with weights): dys[position[t][j]] =
+ * weights[t][j] * dy[t], rows past *kept zeroed, and dweights[t][j] =
+ * <dy[t], ys[position[t][j]]> in fp32, 0 for a dropped choice. */
+int gemm_combine_rows_backward(const void *dy, const void *ys, const int32_t *position,
+                               const int32_t *kept, const float *weights, void *dys,
+                               float *dweights, int64_t tokens, int32_t choices, int64_t cols,
+                               gemm_dtype dtype, void *stream);
+
+typedef enum {
+    /* C[r] = A[r] . B[g] for the rows r of group g: A rows x K, B groups x K x
+     * N, C rows x N; rows past offsets[groups] are zeroed. */
+    GEMM_GROUPED_ROWS = 0,
+    /* The same with B groups x N x K, each matrix transposed: the product of
+     * linear-layer weights, and the gradient of GEMM_GROUPED_ROWS' A. */
+    GEMM_GROUPED_ROWS_BT = 1,
+    /* C[g] = A_g^T . B_g over group g's rows: A rows x K, B rows x N, C groups
+     * x K x N (zero for a group without rows): the gradient of
+     * GEMM_GROUPED_ROWS' B. */
+    GEMM_GROUPED_WGRAD = 2
+} gemm_grouped_op;
+
+/* A grouped product.  dtype is that of A and B (fp32, fp16 or bf16; fp32
+ * accumulation); C is fp32, or the input dtype, rounded to nearest even, with
+ * GEMM_FLAG_C_INPUT_DTYPE (the only flag).  All arrays are dense and
+ * row-major; rows < 2^31 - 1024, K and N < 2^20, 1 <= groups <= 4096.  K = 0
+ * zero-fills C. */
+typedef struct {
+    int32_t op;      /* gemm_grouped_op */
+    int32_t dtype;   /* gemm_dtype */
+    int64_t rows;    /* rows of A, grouped by offsets */
+    int64_t K, N;
+    int32_t groups;
+    uint32_t flags;
+} gemm_grouped;
+
+/* Enqueue a grouped product.  offsets (groups + 1, ascending) is gemm_route's;
+ * workspace (256-byte aligned) needs no clearing and may be NULL when
+ * gemm_grouped_workspace_size() is 0. */
+int gemm_grouped_run(const gemm_grouped *problem, const int32_t *offsets, const void *A,
+                     const void *B, void *C, void *workspace, void *stream);
+
+/* Bytes of workspace gemm_grouped_run needs (0: none). */
+size_t gemm_grouped_workspace_size(const gemm_grouped *problem);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,9 +12,21 @@ from ._lib import (BF16, DP, DTYPES, F16, F32, I8, FLAG_C_INPUT_DTYPE,
                    variants)
 from .plan import FixupError, GemmPlan, matmul, plan_for_device
 
+_ROWS = ("Routing", "route_rows", "gather_rows", "gather_rows_backward", "combine_rows",
+         "combine_rows_backward", "grouped_matmul", "grouped_matmul_wgrad")
+
+
+def __getattr__(name):
+    # these need torch, which the planning and inspection calls do without
+    if name in _ROWS:
+        from . import rows
+        return getattr(rows, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
 __all__ = ["GemmPlan", "FixupError", "matmul", "plan_for_device", "load", "variants",
            "SCHEDULES", "DTYPES", "DP", "PERSISTENT", "STREAMK", "HYBRID", "F32", "F16", "BF16",
            "I8", "FLAG_ONE_TILE", "FLAG_NO_XCD_REMAP", "FLAG_FIXUP_HEAD", "FLAG_FIXUP_SPLIT",
            "FLAG_C_INPUT_DTYPE", "FLAG_DEBUG_DROP_SIGNAL", "FLAG_FIXUP_TWO_KERNEL",
            "FLAG_STREAM_COPIES", "FLAG_PING_PONG", "FLAG_HILBERT_ORDER", "FLAG_RING_KERNEL",
-           "FLAG_TILE_SPLIT", "ROLE_FULL", "ROLE_CONTRIB", "ROLE_OWNER"]
+           "FLAG_TILE_SPLIT", "ROLE_FULL", "ROLE_CONTRIB", "ROLE_OWNER", *_ROWS]

@@ -8,7 +8,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemmsk.so")
-SOURCES = [os.path.join(CSRC, "kernels.hip"), os.path.join(CSRC, "api.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "api.hip", "routing.hip",
+                                           "grouped.hip")]
 ARCH = "gfx950"
 
 

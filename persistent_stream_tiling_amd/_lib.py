@@ -22,6 +22,8 @@ FLAG_TILE_SPLIT = 1 << 13
 ROLE_FULL, ROLE_CONTRIB, ROLE_OWNER = 0, 1, 2
 NOALLOC_MAX_WORKSPACE = 80 << 20  # GEMM_NOALLOC_MAX_WORKSPACE
 
+GROUPED_ROWS, GROUPED_ROWS_BT, GROUPED_WGRAD = 0, 1, 2  # gemm_grouped_op
+
 SCHEDULES = {"dp": DP, "persistent": PERSISTENT, "streamk": STREAMK, "hybrid": HYBRID}
 DTYPES = {"f32": F32, "f16": F16, "bf16": BF16, "i8": I8}
 
@@ -75,12 +77,20 @@ class Segment(ctypes.Structure):
                 ("role", ctypes.c_int32), ("peer_last", ctypes.c_int32)]
 
 
+class Grouped(ctypes.Structure):
+    _fields_ = [("op", ctypes.c_int32), ("dtype", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("groups", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
 EXPORTS = ("gemm_plan_create", "gemm_plan_create_for_device", "gemm_run", "gemm_run_noalloc",
            "gemm_plan_destroy",
            "gemm_plan_workspace_size", "gemm_plan_describe", "gemm_last_error",
            "gemm_plan_get_info", "gemm_plan_segments", "gemm_plan_tile_coords",
            "gemm_plan_logical_wg", "gemm_workspace_status", "gemm_variant_count",
-           "gemm_variant_get")
+           "gemm_variant_get", "gemm_route", "gemm_route_workspace_size", "gemm_gather_rows",
+           "gemm_combine_rows", "gemm_combine_rows_backward", "gemm_grouped_run",
+           "gemm_grouped_workspace_size")
 
 _lib = None
 
@@ -128,6 +138,21 @@ def load(path=None):
     lib.gemm_variant_count.restype = i32
     lib.gemm_variant_get.argtypes = [i32, ctypes.POINTER(VariantInfo)]
     lib.gemm_variant_get.restype = ctypes.c_int
+    lib.gemm_route.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp, vp, vp]
+    lib.gemm_route.restype = ctypes.c_int
+    lib.gemm_route_workspace_size.argtypes = [i64, i32, i32]
+    lib.gemm_route_workspace_size.restype = ctypes.c_size_t
+    lib.gemm_gather_rows.argtypes = [vp, vp, vp, vp, i64, i32, i64, ctypes.c_int, vp]
+    lib.gemm_gather_rows.restype = ctypes.c_int
+    lib.gemm_combine_rows.argtypes = [vp, vp, vp, vp, i64, i32, i64, ctypes.c_int, vp]
+    lib.gemm_combine_rows.restype = ctypes.c_int
+    lib.gemm_combine_rows_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i64,
+                                               ctypes.c_int, vp]
+    lib.gemm_combine_rows_backward.restype = ctypes.c_int
+    lib.gemm_grouped_run.argtypes = [ctypes.POINTER(Grouped), vp, vp, vp, vp, vp, vp]
+    lib.gemm_grouped_run.restype = ctypes.c_int
+    lib.gemm_grouped_workspace_size.argtypes = [ctypes.POINTER(Grouped)]
+    lib.gemm_grouped_workspace_size.restype = ctypes.c_size_t
     _lib = lib
     return lib
 

@@ -13,11 +13,24 @@
 #include <new>
 #include <string>
 
+#include "errors.h"
 #include "gemm_sk.h"
 #include "kernels.h"
 #include "schedule.h"
 
 using namespace gsk;
+
+static thread_local std::string g_error;
+
+void gsk::set_error(const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_error = buf;
+}
 
 struct gemm_plan {
     int64_t M, N, K;
@@ -39,18 +52,6 @@ struct gemm_plan {
 };
 
 namespace {
-
-thread_local std::string g_error;
-
-void set_error(const char *fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_error = buf;
-}
 
 int elem_size(int dtype) { return dtype == GEMM_F32 ? 4 : (dtype == GEMM_I8 ? 1 : 2); }
 

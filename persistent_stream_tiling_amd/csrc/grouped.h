@@ -1,0 +1,112 @@
+// Shared by the kernels of the products whose rows choose their matrix: the
+// argument block, and how a workgroup finds its tile from the group offsets.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace gsk {
+
+// One launch of C[r] = A[r] . B[group of r] (rows sorted by group, group g
+// owning rows offsets[g] .. offsets[g + 1] - 1), or of its weight gradient
+// C[g] = A_g^T . D_g.
+struct GroupedArgs {
+    const uint8_t *A;
+    const uint8_t *B;        // rows product: groups matrices; weight gradient: D
+    uint8_t *C;
+    const int32_t *offsets;  // groups + 1
+    int64_t b_stride;        // elements between groups of B (rows product)
+    int32_t rows;            // rows of A
+    int32_t groups;
+    int32_t M;               // weight gradient: columns of A (= rows of C[g])
+    int32_t N, K;            // rows product: C columns, depth
+    int32_t lda, ldb;        // leading dimensions in elements
+    int32_t c_dtype;         // 0 fp32, 1 fp16, 2 bf16
+    int32_t c_vec;           // C's rows hold whole aligned 4-element vectors
+    int32_t tiles_n, tiles_m;// tiles_m: weight gradient only
+    int32_t xcds;
+};
+
+// First row of group g, kept inside [0, rows] whatever the buffer holds.
+__device__ __forceinline__ int32_t group_start(const int32_t *offsets, int32_t g, int32_t rows)
+{
+    const int32_t o = offsets[g];
+    return o < 0 ? 0 : (o < rows ? o : rows);
+}
+
+// Rows [lo, hi) of group g; g = groups stands for the rows past the last
+// group, which are zeroed.
+__device__ __forceinline__ void group_rows(const int32_t *offsets, int32_t g, int32_t groups,
+                                           int32_t rows, int32_t *lo, int32_t *hi)
+{
+    const int32_t a = group_start(offsets, g, rows);
+    const int32_t b = g < groups ? group_start(offsets, g + 1, rows) : rows;
+    *lo = a;
+    *hi = b > a ? b : a;
+}
+
+struct RowTile {
+    int32_t g;     // group, or `groups` for the rows past the last one
+    int32_t m0;    // first row
+    int32_t m_end; // end of the group's rows
+    int32_t tn;    // column tile
+};
+
+// Tile of hardware workgroup hw out of `launched`.  The host knows only an
+// upper bound of the number of tiles, so each wave counts them from the
+// offsets: every lane takes a run of groups, a scan over the lanes gives the
+// total, and the lane whose run holds the wanted tile walks it.  Tiles are
+// numbered by group, then row tile, then column tile; each die takes one
+// contiguous run of the true total (workgroup ids are dealt to the dies in
+// turn), so a group's matrix is read into one die's L2, or two.  False: no
+// tile for this workgroup.
+template <int BM>
+__device__ __forceinline__ bool find_row_tile(const GroupedArgs &a, int64_t hw, RowTile *out)
+{
+    const int lane = threadIdx.x & 63;
+    const int32_t runs = a.groups + 1;  // with the rows past the last group
+    const int32_t each = (runs + 63) >> 6;
+    const int32_t g_lo = lane * each;
+    const int32_t g_hi = g_lo + each < runs ? g_lo + each : runs;
+    int32_t mine = 0;  // row tiles of the lane's groups (at most rows + groups)
+    for (int32_t g = g_lo; g < g_hi; ++g) {
+        int32_t lo, hi;
+        group_rows(a.offsets, g, a.groups, a.rows, &lo, &hi);
+        mine += (int32_t)(((int64_t)hi - lo + BM - 1) / BM);
+    }
+    int32_t sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int32_t up = __shfl_up(sum, d);
+        sum += lane >= d ? up : 0;
+    }
+    const int64_t total = (int64_t)__builtin_amdgcn_readlane(sum, 63) * a.tiles_n;
+    const int64_t share = (total + a.xcds - 1) / a.xcds;
+    const int64_t die = hw % a.xcds, nth = hw / a.xcds;
+    const int64_t id = die * share + nth;
+    if (nth >= share || id >= total)
+        return false;
+    const int32_t rt = (int32_t)(id / a.tiles_n);
+    const uint64_t past = __builtin_amdgcn_ballot_w64(sum > rt);
+    if (!past)  // (offsets that do not ascend can make the sums wrap)
+        return false;
+    const int owner = __builtin_ctzll(past);
+    // the owner lane walks its groups; every lane follows with its values
+    int32_t at = __builtin_amdgcn_readlane(sum - mine, owner);
+    int32_t g = owner * each, lo = 0, hi = 0;
+    for (;; ++g) {
+        group_rows(a.offsets, g, a.groups, a.rows, &lo, &hi);
+        const int32_t n = (int32_t)(((int64_t)hi - lo + BM - 1) / BM);
+        if (rt < at + n || g + 1 >= runs)
+            break;
+        at += n;
+    }
+    out->g = g;
+    out->m0 = lo + (rt - at) * BM;
+    out->m_end = hi;
+    out->tn = (int32_t)(id - (int64_t)rt * a.tiles_n);
+    return true;
+}
+
+}  // namespace gsk

@@ -1,0 +1,264 @@
+"""Products whose rows choose their matrix: routing rows to groups and back, and
+the groups' products with their gradients (argument marshalling only).
+
+A mixture-of-experts layer over ``x`` (tokens x K) with router choices ``ids``
+and ``weights`` (tokens x choices) and expert matrices ``w`` (groups x K x N):
+
+    r = route_rows(ids, groups)
+    xs = gather_rows(x, r)
+    ys = grouped_matmul(xs, w, r.offsets, out_dtype=x.dtype)
+    y = combine_rows(ys, weights, r)
+
+and its gradients from ``dy``:
+
+    dys, dweights = combine_rows_backward(dy, ys, weights, r)
+    dw = grouped_matmul_wgrad(xs, dys, r.offsets)
+    dxs = grouped_matmul(dys, w.transpose(1, 2), r.offsets, out_dtype=x.dtype)
+    dx = gather_rows_backward(dxs, r)
+
+Nothing here reads the GPU: group sizes stay there, and every call can be
+captured into a graph.  Outputs and workspaces come from torch's allocator on
+the current stream, which is the stream each call runs on; tensors made on
+another stream need that stream's usual synchronization and
+``record_stream``.
+"""
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from ._lib import (BF16, F16, F32, FLAG_C_INPUT_DTYPE, GROUPED_ROWS, GROUPED_ROWS_BT,
+                   GROUPED_WGRAD, Grouped, last_error, load)
+
+_CODES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+
+
+@dataclass(frozen=True)
+class Routing:
+    """Entries (token, choice) sorted by group, as ``route_rows`` makes it:
+    ``offsets`` (groups + 1; group g owns sorted rows offsets[g] ..
+    offsets[g + 1] - 1), ``order`` (the entry at each sorted row, -1 past the
+    kept ones) and ``position`` (tokens x choices: an entry's sorted row, -1 if
+    it was dropped), int32 on the GPU."""
+    offsets: torch.Tensor
+    order: torch.Tensor
+    position: torch.Tensor
+
+    def __post_init__(self):
+        _gpu("a routing", self.offsets, self.order, self.position)
+        for t in (self.offsets, self.order, self.position):
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError("a routing holds contiguous int32 tensors")
+        if self.offsets.dim() != 1 or self.offsets.numel() < 2 or self.position.dim() != 2 or \
+                self.order.shape != (self.position.numel(),):
+            raise ValueError("a routing holds offsets (groups + 1), order (tokens * choices) and "
+                             "position (tokens x choices)")
+
+    @property
+    def groups(self):
+        return self.offsets.numel() - 1
+
+    @property
+    def kept(self):
+        """Address of the number of rows kept, offsets[groups]."""
+        return self.offsets.data_ptr() + 4 * (self.offsets.numel() - 1)
+
+
+def _gpu(what, *tensors):
+    dev = tensors[0].device
+    for t in tensors:
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"{what}: all tensors must be on one GPU")
+    return dev
+
+
+def _call(dev, fn, *args):
+    """fn(*args, stream) on the device's current stream; raises on an error."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(dev, fn, *args)
+    rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != 0:
+        kind = ValueError if rc == -1 else RuntimeError
+        raise kind(f"{fn.__name__} failed ({rc}): {last_error()}")
+
+
+def _code(t, what):
+    if t.dtype not in _CODES:
+        raise ValueError(f"{what} must be float32, float16 or bfloat16, got {t.dtype}")
+    return _CODES[t.dtype]
+
+
+def _c_flags(dtype, out_dtype):
+    """(torch dtype of C, plan flags) as ``matmul``: fp32, or the input dtype."""
+    if out_dtype not in (None, torch.float32, dtype):
+        raise ValueError(f"out_dtype must be float32 or {dtype}, got {out_dtype}")
+    half = out_dtype == dtype and dtype != torch.float32
+    return (dtype if half else torch.float32), (FLAG_C_INPUT_DTYPE if half else 0)
+
+
+def _bytes(n, dev):
+    return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def route_rows(ids, groups):
+    """Sort the entries of ``ids`` (tokens x choices, or one choice per token:
+    int32 or int64 on the GPU) stably by group; an id outside [0, groups) drops
+    its entry.  Returns a ``Routing``."""
+    dev = _gpu("route_rows", ids)
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    if ids.dim() == 1:
+        ids = ids.unsqueeze(1)
+    if ids.dim() != 2 or ids.shape[1] < 1:
+        raise ValueError(f"ids must be tokens x choices, got {tuple(ids.shape)}")
+    groups = int(groups)
+    if groups < 1:
+        raise ValueError(f"groups must be at least 1, got {groups}")
+    lib = load()
+    ids = ids.contiguous()
+    T, k = ids.shape
+    offsets = torch.empty(groups + 1, dtype=torch.int32, device=dev)
+    order = torch.empty(T * k, dtype=torch.int32, device=dev)
+    position = torch.empty((T, k), dtype=torch.int32, device=dev)
+    ws = _bytes(lib.gemm_route_workspace_size(T, k, groups), dev)
+    _call(dev, lib.gemm_route, ids.data_ptr(), ids.element_size(), T, k, groups,
+          offsets.data_ptr(), order.data_ptr(), position.data_ptr(), _ptr(ws))
+    return Routing(offsets, order, position)
+
+
+def _rows(what, t, n, cols=None):
+    if t.dim() != 2 or t.shape[0] != n or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{what} must have {n} rows" +
+                         (f" of {cols}" if cols is not None else "") + f", got {tuple(t.shape)}")
+    _code(t, what)
+    return t.contiguous()
+
+
+def gather_rows(x, routing):
+    """The rows of ``x`` (tokens x cols) in sorted order: tokens * choices rows,
+    those past the kept ones zero."""
+    dev = _gpu("gather_rows", x, routing.position)
+    T, k = routing.position.shape
+    x = _rows("x", x, T)
+    xs = torch.empty((T * k, x.shape[1]), dtype=x.dtype, device=dev)
+    _call(dev, load().gemm_gather_rows, x.data_ptr(), routing.position.data_ptr(), routing.kept,
+          xs.data_ptr(), T, k, x.shape[1], _CODES[x.dtype])
+    return xs
+
+
+def gather_rows_backward(dxs, routing):
+    """The gradient of ``gather_rows``: each token's sum of its kept choices'
+    rows, in fp32 and rounded once."""
+    return _combine("gather_rows_backward", dxs, None, routing)
+
+
+def combine_rows(ys, weights, routing):
+    """y[t] = sum_j weights[t, j] * ys[row of (t, j)] over t's kept choices, in
+    fp32 and rounded once; ``weights`` (tokens x choices) is float32."""
+    return _combine("combine_rows", ys, _weights("combine_rows", weights, routing), routing)
+
+
+def _weights(what, weights, routing):
+    if weights.dtype != torch.float32 or weights.shape != routing.position.shape:
+        raise ValueError(f"{what}: weights must be float32 and {tuple(routing.position.shape)}, "
+                         f"got {weights.dtype} {tuple(weights.shape)}")
+    _gpu(what, weights, routing.position)
+    return weights.contiguous()
+
+
+def _combine(what, ys, weights, routing):
+    dev = _gpu(what, ys, routing.position)
+    T, k = routing.position.shape
+    ys = _rows("the sorted rows", ys, T * k)
+    y = torch.empty((T, ys.shape[1]), dtype=ys.dtype, device=dev)
+    _call(dev, load().gemm_combine_rows, ys.data_ptr(), routing.position.data_ptr(),
+          _ptr(weights), y.data_ptr(), T, k, ys.shape[1], _CODES[ys.dtype])
+    return y
+
+
+def combine_rows_backward(dy, ys, weights, routing):
+    """The gradients of ``combine_rows`` from ``dy`` (tokens x cols): ``dys``
+    in sorted order (rows past the kept ones zero) and ``dweights`` (float32,
+    zero for a dropped choice)."""
+    what = "combine_rows_backward"
+    weights = _weights(what, weights, routing)
+    dev = _gpu(what, dy, ys, routing.position)
+    T, k = routing.position.shape
+    ys = _rows("the sorted rows", ys, T * k)
+    dy = _rows("dy", dy, T, ys.shape[1])
+    if dy.dtype != ys.dtype:
+        raise ValueError(f"dy and the sorted rows differ in dtype: {dy.dtype}, {ys.dtype}")
+    dys = torch.empty_like(ys)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _call(dev, load().gemm_combine_rows_backward, dy.data_ptr(), ys.data_ptr(),
+          routing.position.data_ptr(), routing.kept, weights.data_ptr(), dys.data_ptr(),
+          dweights.data_ptr(), T, k, ys.shape[1], _CODES[ys.dtype])
+    return dys, dweights
+
+
+def _offsets(what, offsets, groups=None):
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or \
+            (groups is not None and offsets.numel() != groups + 1):
+        raise ValueError(f"{what}: offsets must be int32 and hold groups + 1"
+                         f"{'' if groups is None else f' = {groups + 1}'} values, got "
+                         f"{offsets.dtype} {tuple(offsets.shape)}")
+    return offsets.contiguous()
+
+
+def _grouped(dev, op, a, b, c, offsets, K, N, groups, flags):
+    lib = load()
+    p = Grouped(op, _CODES[a.dtype], a.shape[0], K, N, groups, flags)
+    ws = _bytes(lib.gemm_grouped_workspace_size(ctypes.byref(p)), dev)
+    _call(dev, lib.gemm_grouped_run, ctypes.byref(p), offsets.data_ptr(), a.data_ptr(),
+          b.data_ptr(), c.data_ptr(), _ptr(ws))
+    return c
+
+
+def grouped_matmul(a, b, offsets, out_dtype=None):
+    """C[r] = a[r] @ b[g] for the rows r of group g (offsets[g] ..
+    offsets[g + 1] - 1); rows past the last group are zero.  ``a`` is rows x K,
+    ``b`` groups x K x N: contiguous, or the transposed view of a contiguous
+    groups x N x K tensor (linear-layer weights, or the input gradient
+    ``grouped_matmul(dc, b.transpose(1, 2), offsets)``), which is read as it
+    lies; other layouts are copied first.  C is fp32, or a's dtype when
+    ``out_dtype`` is a's dtype."""
+    dev = _gpu("grouped_matmul", a, b, offsets)
+    if a.dim() != 2 or b.dim() != 3 or a.shape[1] != b.shape[1]:
+        raise ValueError(f"incompatible shapes {tuple(a.shape)} and {tuple(b.shape)}")
+    if a.dtype != b.dtype:
+        raise ValueError(f"a and b differ in dtype: {a.dtype}, {b.dtype}")
+    _code(a, "a")
+    offsets = _offsets("grouped_matmul", offsets, b.shape[0])
+    c_type, flags = _c_flags(a.dtype, out_dtype)
+    a = a.contiguous()
+    op, bt = GROUPED_ROWS, b.transpose(1, 2)
+    if not b.is_contiguous() and bt.is_contiguous():
+        op, b = GROUPED_ROWS_BT, bt
+    else:
+        b = b.contiguous()
+    K, N = bt.shape[2], bt.shape[1]
+    c = torch.empty((a.shape[0], N), dtype=c_type, device=dev)
+    return _grouped(dev, op, a, b, c, offsets, K, N, b.shape[0], flags)
+
+
+def grouped_matmul_wgrad(a, dc, offsets, out_dtype=None):
+    """The gradient of ``grouped_matmul``'s b from dc: a[rows of g].T @
+    dc[rows of g] for every group g (groups x K x N; zero for a group without
+    rows), fp32 or, with ``out_dtype``, a's dtype."""
+    dev = _gpu("grouped_matmul_wgrad", a, dc, offsets)
+    if a.dim() != 2 or dc.dim() != 2 or a.shape[0] != dc.shape[0]:
+        raise ValueError(f"incompatible shapes {tuple(a.shape)} and {tuple(dc.shape)}")
+    if a.dtype != dc.dtype:
+        raise ValueError(f"a and dc differ in dtype: {a.dtype}, {dc.dtype}")
+    _code(a, "a")
+    offsets = _offsets("grouped_matmul_wgrad", offsets)
+    c_type, flags = _c_flags(a.dtype, out_dtype)
+    a, dc = a.contiguous(), dc.contiguous()
+    groups, K, N = offsets.numel() - 1, a.shape[1], dc.shape[1]
+    c = torch.empty((groups, K, N), dtype=c_type, device=dev)
+    return _grouped(dev, GROUPED_WGRAD, a, dc, c, offsets, K, N, groups, flags)

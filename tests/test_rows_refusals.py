@@ -1,0 +1,138 @@
+"""What the operators whose rows choose their matrix refuse, without a GPU: the
+C calls check every argument before they launch anything, so addresses that
+point nowhere serve here."""
+import ctypes
+
+import pytest
+import torch
+
+import persistent_stream_tiling_amd as gsk
+from persistent_stream_tiling_amd import _lib
+from persistent_stream_tiling_amd._lib import Grouped, last_error
+
+P = 0x1000  # an aligned address that nothing reads
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return gsk.load()
+
+
+def refused(rc, text, code=-1):
+    assert rc == code
+    assert text in last_error(), last_error()
+
+
+def test_route_refuses(lib):
+    ok = dict(ids=P, id_bytes=4, tokens=8, choices=2, groups=4, offsets=P, order=P, position=P,
+              ws=None)
+
+    def run(**kw):
+        a = {**ok, **kw}
+        return lib.gemm_route(a["ids"], a["id_bytes"], a["tokens"], a["choices"], a["groups"],
+                              a["offsets"], a["order"], a["position"], a["ws"], None)
+
+    refused(run(tokens=-1), "must not be negative")
+    refused(run(choices=0), "choices >= 1")
+    refused(run(tokens=2 ** 30, choices=2), "below 2^31")
+    refused(run(groups=0), "groups must be between 1 and 16382")
+    refused(run(groups=16383), "groups must be between")
+    refused(run(id_bytes=2), "int32 or int64")
+    for name in ("ids", "offsets", "order", "position"):
+        refused(run(**{name: None}), "NULL")
+        refused(run(**{name: P + 2}), "misaligned")
+    refused(run(ids=P + 4, id_bytes=8), "misaligned")
+    # more than one workgroup's entries: the counts need a workspace
+    assert lib.gemm_route_workspace_size(4096, 2, 4) > 0
+    refused(run(tokens=4096), "bytes of workspace", -2)
+
+
+def test_route_workspace_size(lib):
+    assert lib.gemm_route_workspace_size(64, 8, 128) == 0
+    assert lib.gemm_route_workspace_size(0, 8, 128) == 0
+    assert lib.gemm_route_workspace_size(8192, 8, 64) == 16 * 65 * 4
+    # at most 256 workgroups, however many entries
+    assert lib.gemm_route_workspace_size(2 ** 28 - 1, 8, 64) <= 256 * 65 * 4
+    assert lib.gemm_route_workspace_size(-1, 8, 64) == 0
+
+
+def test_row_copies_refuse(lib):
+    def gather(x=P, position=P, kept=P, xs=P, tokens=8, choices=2, cols=16, dtype=_lib.BF16):
+        return lib.gemm_gather_rows(x, position, kept, xs, tokens, choices, cols, dtype, None)
+
+    def combine(ys=P, position=P, weights=P, y=P, tokens=8, choices=2, cols=16, dtype=_lib.BF16):
+        return lib.gemm_combine_rows(ys, position, weights, y, tokens, choices, cols, dtype, None)
+
+    def back(dy=P, ys=P, position=P, kept=P, weights=P, dys=P, dweights=P, tokens=8, choices=2,
+             cols=16, dtype=_lib.BF16):
+        return lib.gemm_combine_rows_backward(dy, ys, position, kept, weights, dys, dweights,
+                                              tokens, choices, cols, dtype, None)
+
+    names = {gather: ("x", "position", "kept", "xs"), combine: ("ys", "position", "y"),
+             back: ("dy", "ys", "position", "kept", "weights", "dys", "dweights")}
+    for f, args in names.items():
+        refused(f(tokens=-1), "must not be negative")
+        refused(f(cols=-1), "must not be negative")
+        refused(f(choices=0), "choices >= 1")
+        refused(f(tokens=2 ** 30), "below 2^31")
+        refused(f(cols=2 ** 22), "cols must stay below")
+        refused(f(dtype=_lib.I8), "fp32, fp16 or bf16")
+        refused(f(dtype=9), "fp32, fp16 or bf16")
+        for name in args:
+            refused(f(**{name: None}), "NULL")
+            refused(f(**{name: P + 1}), "misaligned")
+        assert f(tokens=0) == 0  # nothing to do
+    refused(gather(x=P + 2, dtype=_lib.F32), "misaligned")
+    assert gather(cols=0) == 0 and combine(cols=0) == 0
+
+
+def test_grouped_refuses(lib):
+    def run(op=0, dtype=_lib.BF16, rows=64, K=32, N=16, groups=4, flags=0, offsets=P, A=P, B=P,
+            C=P):
+        p = Grouped(op, dtype, rows, K, N, groups, flags)
+        return lib.gemm_grouped_run(ctypes.byref(p), offsets, A, B, C, None, None)
+
+    refused(lib.gemm_grouped_run(None, P, P, P, P, None, None), "NULL problem")
+    refused(run(op=3), "unknown grouped product")
+    refused(run(op=-1), "unknown grouped product")
+    refused(run(dtype=_lib.I8), "fp32, fp16 or bf16")
+    refused(run(flags=_lib.FLAG_FIXUP_SPLIT), "GEMM_FLAG_C_INPUT_DTYPE")
+    for kw in (dict(rows=-1), dict(K=-1), dict(N=-1), dict(groups=0)):
+        refused(run(**kw), "must not be negative")
+    refused(run(groups=4097), "at most 4096")
+    refused(run(rows=2 ** 31 - 1024), "rows must stay below")
+    refused(run(K=2 ** 20), "K and N below")
+    refused(run(N=2 ** 20), "K and N below")
+    for name in ("offsets", "A", "B", "C"):
+        refused(run(**{name: None}), "NULL")
+        refused(run(**{name: P + 1}), "misaligned")
+    refused(run(dtype=_lib.F32, A=P + 2), "misaligned")
+    refused(run(rows=2 ** 31 - 2048, N=2 ** 20 - 1), "too many tiles")
+    assert run(rows=0, A=None, B=None, C=None) == 0
+    assert run(N=0, B=None, C=None) == 0
+    assert run(op=2, K=0, A=None, C=None) == 0
+
+
+def test_struct_layout_matches_the_header(tmp_path):
+    import os
+    import subprocess
+    src = tmp_path / "sizes.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "gemm_sk.h"\nint main(void)'
+                   '{printf("%zu %zu %zu", sizeof(gemm_grouped), offsetof(gemm_grouped, rows), '
+                   'offsetof(gemm_grouped, flags)); return 0;}')
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o",
+                    str(tmp_path / "sizes")], check=True)
+    got = subprocess.run([str(tmp_path / "sizes")], capture_output=True, text=True).stdout.split()
+    assert [int(v) for v in got] == [ctypes.sizeof(Grouped), Grouped.rows.offset,
+                                     Grouped.flags.offset]
+
+
+def test_python_calls_refuse_tensors_off_the_gpu():
+    x, ids = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    w, off = torch.zeros(3, 8, 5), torch.zeros(4, dtype=torch.int32)
+    for call in (lambda: gsk.route_rows(ids, 3), lambda: gsk.Routing(off, off, ids),
+                 lambda: gsk.grouped_matmul(x, w, off),
+                 lambda: gsk.grouped_matmul_wgrad(x, x, off)):
+        with pytest.raises(ValueError, match="on one GPU"):
+            call()
