@@ -486,8 +486,9 @@ typedef struct {
 } gemm_grouped;
 
 /* Enqueue a grouped product.  offsets (groups + 1, ascending) is gemm_route's;
- * workspace (256-byte aligned) needs no clearing and may be NULL when
- * gemm_grouped_workspace_size() is 0. */
+ * A and B are 16-byte aligned; workspace (256-byte aligned) needs no clearing
+ * and may be NULL when gemm_grouped_workspace_size() is 0: it holds fp16/bf16
+ * operands whose rows are no multiple of 16 bytes, repacked. */
 int gemm_grouped_run(const gemm_grouped *problem, const int32_t *offsets, const void *A,
                      const void *B, void *C, void *workspace, void *stream);
 

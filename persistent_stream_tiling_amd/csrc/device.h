@@ -15,6 +15,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
 constexpr uint32_t kOutOfRange = 0x80000000u;  // a buffer offset that is never in range
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base)
@@ -71,6 +74,114 @@ __device__ __forceinline__ void store_four(const f32x4 &v, __amdgpu_buffer_rsrc_
             __builtin_amdgcn_raw_buffer_store_b32(
                 u[e], c, (int)(ok && n + e < N ? off + 4 * e : kOutOfRange), 0, 0);
     }
+}
+
+// One 32x32 accumulator block (rows brow .., columns col .. of C; rows_ok: how
+// many rows from the descriptor's base exist).  Lane l holds row brow + l % 32
+// at columns col + 8g + 4(l / 32) + e in register 4g + e.  For vector stores,
+// quads 2j and 2j + 1 are exchanged first (v_permlane16_swap: lanes 16-31 and
+// 48-63 of the one with lanes 0-15 and 32-47 of the other), so that each store
+// covers 16 rows with 64 contiguous bytes (32 for 16-bit C) instead of 32 rows
+// with 32.
+__device__ __forceinline__ void store_block(const f32x16 &blk, __amdgpu_buffer_rsrc_t c,
+                                            uint32_t row_bytes, int brow, int rows_ok, int col,
+                                            int N, bool vec, int c_dtype)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const f32x4 q0 = f32x4{blk[8 * j], blk[8 * j + 1], blk[8 * j + 2], blk[8 * j + 3]};
+        const f32x4 q1 = f32x4{blk[8 * j + 4], blk[8 * j + 5], blk[8 * j + 6], blk[8 * j + 7]};
+        if (vec) {
+            f32x4 lo, hi;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const auto r =
+                    __builtin_amdgcn_permlane16_swap(bits_of(q0[e]), bits_of(q1[e]), false, false);
+                lo[e] = __builtin_bit_cast(float, (uint32_t)r[0]);
+                hi[e] = __builtin_bit_cast(float, (uint32_t)r[1]);
+            }
+            const int row = brow + (lane & 15);
+            const int n = col + 16 * j + 8 * ((lane >> 4) & 1) + 4 * (lane >> 5);
+            store_four(lo, c, (uint32_t)row * row_bytes, n, N, row < rows_ok, true, c_dtype);
+            store_four(hi, c, (uint32_t)(row + 16) * row_bytes, n, N, row + 16 < rows_ok, true,
+                       c_dtype);
+        } else {
+            const int row = brow + (lane & 31), n = col + 16 * j + 4 * (lane >> 5);
+            store_four(q0, c, (uint32_t)row * row_bytes, n, N, row < rows_ok, false, c_dtype);
+            store_four(q1, c, (uint32_t)row * row_bytes, n + 8, N, row < rows_ok, false, c_dtype);
+        }
+    }
+}
+
+// ---- direct global -> LDS copies and the rings they fill
+
+__device__ __forceinline__ void barrier_only()
+{
+    // no memory fence: the callers' s_waitcnt order what they need; the asm
+    // keeps the compiler from moving LDS accesses across it
+    asm volatile("s_barrier" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void wait_lds()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
+// A raw buffer descriptor (base, no stride, 2^31 - 1 bytes, untyped) as words.
+__device__ __forceinline__ i32x4 rsrc_words(const void *base)
+{
+    const uint64_t b = (uint64_t)base;
+    return i32x4{(int)(uint32_t)b, (int)((uint32_t)(b >> 32) & 0xffff), 0x7fffffff, 0x00020000};
+}
+
+// 16 bytes per lane from buffer offset voff (kOutOfRange: zeros) into LDS at
+// lds_addr + 16 * lane (lds_addr wave-uniform).  Inline assembly, so that the
+// compiler does not wait for every copy in flight before each transposing LDS
+// read; the callers' s_waitcnt vmcnt() and barriers order the copies.
+__device__ __forceinline__ void copy16(i32x4 rsrc, uint32_t voff, uint32_t lds_addr)
+{
+    asm volatile("s_mov_b32 m0, %0\n\t"
+                 "s_nop 0\n\t"
+                 "buffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voff), "s"(rsrc)
+                 : "m0");
+}
+
+#define GSK_LDS_PTR(T, p) ((__attribute__((address_space(3))) T *)(p))
+
+__device__ __forceinline__ uint32_t lds_address(const uint8_t *p)
+{
+    return (uint32_t)(uintptr_t)GSK_LDS_PTR(const uint8_t, p);
+}
+
+// 16-byte chunk c of a 128-byte LDS row r sits at c ^ swz_row(r): eight rows
+// read at one chunk index then touch all 32 bank pairs.
+__device__ __forceinline__ uint32_t swz_row(int row) { return (uint32_t)(row ^ (row >> 3)) & 7; }
+
+// Chunk c of k-row r of a slab stored k-row by k-row sits at c ^ swz_krow(r)
+// ({0, 6, 10, 12} by r mod 4): the four k-rows that one half of a transposing
+// read touches fall on distinct banks.
+__device__ __forceinline__ uint32_t swz_krow(int krow) { return (0xCA60u >> ((krow & 3) * 4)) & 0xF; }
+
+// acc += a . b^T for one 16-deep step of a 32x32 block, operands swapped so
+// that the accumulator holds the transposed block (see store_block).
+template <int DT>
+__device__ __forceinline__ void mfma16(f32x16 &acc, const u32x4 &b, const u32x4 &a)
+{
+    if constexpr (DT == 1)
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b),
+                                                     __builtin_bit_cast(f16x8, a), acc, 0, 0, 0);
+    else
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b),
+                                                      __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
 }
 
 }  // namespace dev

@@ -10,6 +10,7 @@
 #include "errors.h"
 #include "gemm_sk.h"
 #include "grouped.h"
+#include "kernels.h"
 
 namespace gsk {
 
@@ -18,8 +19,7 @@ using namespace dev;
 namespace {
 
 // ---------------------------------------------------------------------------
-// Exact-product kernel: operands are widened to fp32 in LDS and multiplied by
-// the fp32 matrix instruction, 128x128 tiles, any sizes and alignments.
+// fp32: the fp32 matrix instruction, 128x128 tiles, any sizes and alignments.
 //
 // An operand is a slab of 128 rows (m or n) by 16 k per iteration.  It lies in
 // memory either with k contiguous (KC: 8 consecutive k per thread) or with
@@ -189,6 +189,283 @@ __global__ __launch_bounds__(kXThreads) void wgrad_exact_kernel(GroupedArgs a)
                 a.N, a.c_dtype, a.c_vec);
 }
 
+// ---------------------------------------------------------------------------
+// fp16 / bf16, 256x256 tiles, eight waves in two groups that take turns.
+//
+// Group 0 (waves 0-3) computes tile rows 0-127, group 1 (waves 4-7) rows
+// 128-255, each wave a 128 x 64 block; wave q of both groups runs on the same
+// SIMD.  Time is cut into phases between workgroup barriers.  With
+// half-iterations h (32 k each):
+//   phase 2h:     group 0 multiplies h (16 MFMAs, operands in registers);
+//                 group 1 copies its operand's piece h + 3 and reads h;
+//   phase 2h + 1: group 1 multiplies h;
+//                 group 0 copies its operand's piece h + 4 and reads h + 1
+// (group 0 reads h = 0 in a phase of its own before phase 0).  Group 0 copies
+// operand A, group 1 operand B, straight from global memory into LDS, in
+// pieces of 16 KiB: four 1 KiB copies per wave.
+//
+// An operand lies in memory in one of two ways, and its pieces with it:
+//   LINES   k contiguous.  Piece c holds 128 of the tile's 256 rows (those of
+//           parity c & 1) by the 64 k of iteration c >> 1, in whole 128-byte
+//           lines; fragments are 16-byte reads.  Ring of 5 pieces.
+//   KROWS   m or n contiguous.  Piece c holds the 32 k-rows of half-iteration
+//           c by all 256 columns; fragments are transposing reads.  Ring of 4.
+// So the product with B as it lies (A LINES, B KROWS), with B transposed
+// (LINES, LINES) and the weight gradient (KROWS, KROWS) are one kernel, none
+// with a transposing pass over memory, in at most 160 KiB of LDS.
+//
+// Why the rings are long enough.  Every phase ends with a wait for the
+// wave's own copies (at most two pieces' in flight; one for B in LINES), for
+// the LDS reads it issued, and a barrier.  Copied by group 0, piece c is issued
+// in phase 2c - 7 and landed by the end of 2c - 3; by group 1, in 2c - 6,
+// landed by the end of 2c - 2 (2c - 4 with one in flight).  First reads:
+//   A LINES  even pieces by group 0 in phase 2c - 1, odd by group 1 in 2c - 2
+//   A KROWS  2c - 1          B KROWS  2c - 1
+//   B LINES  odd pieces by group 0 in 2c - 3, even in 2c - 1
+// and the piece that c overwrites was last read in
+//   A LINES  2c - 9 (even; c - 5)   or 2c - 10 (odd)
+//   A KROWS  2c - 8 (c - 4)         B KROWS  2c - 8 (c - 4)
+//   B LINES  2c - 8 (c - 5, even)   or 2c - 10 (odd)
+// each before the copy's phase.  Copies past the end of k read nothing
+// (out-of-range offsets) and zero a free piece, so the wait counts are
+// constants.
+enum { LINES = 0, KROWS = 1 };
+
+constexpr int kBig = 256, kPiece = 16384;
+
+constexpr int ring_of(int layout) { return layout == LINES ? 5 : 4; }
+
+// What one workgroup multiplies: the tile's corner in both operands.
+struct TileWork {
+    const uint8_t *a, *b;  // LINES: row 0, k 0.  KROWS: k-row 0, column 0
+    int64_t lda, ldb;      // elements
+    int m, n, k;           // rows and columns that exist from the corner on; depth
+};
+
+template <int DT, int LA, int LB, int GRP>
+__device__ __forceinline__ void big_tile_group(f32x16 (&acc)[4][2], const TileWork &w, uint8_t *lds,
+                                               int q)
+{
+    constexpr int LX = GRP == 0 ? LA : LB;  // layout of the operand this group copies
+    constexpr int RA = ring_of(LA), RB = ring_of(LB);
+    constexpr int B_BASE = RA * kPiece;
+    const int lane = threadIdx.x & 63;
+    const int half = lane >> 5, l32 = lane & 31;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
+
+    // Copies: copy j of this wave fills KiB 4j + q of a piece.
+    const uint8_t *x = GRP == 0 ? w.a : w.b;
+    const int64_t ldx = GRP == 0 ? w.lda : w.ldb;
+    const int have = GRP == 0 ? w.m : w.n;  // rows (LINES) or columns (KROWS) that exist
+    int cp_row[4], cp_chunk[4];
+    uint32_t off0[4], off1[4];  // LINES: even and odd pieces
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (LX == LINES) {
+            cp_row[j] = 8 * (4 * j + q) + (lane >> 3);
+            cp_chunk[j] = (lane & 7) ^ (int)swz_row(cp_row[j]);
+            const uint32_t o = (uint32_t)(cp_row[j] * (int)ldx * 2 + (cp_chunk[j] << 4));
+            off0[j] = cp_row[j] < have ? o : kOutOfRange;
+            off1[j] = cp_row[j] + 128 < have ? o + (uint32_t)(256 * (int)ldx) : kOutOfRange;
+        } else {
+            cp_row[j] = 2 * (4 * j + q) + (lane >> 5);
+            cp_chunk[j] = (lane & 31) ^ (int)swz_krow(cp_row[j]);
+            off0[j] = cp_chunk[j] * 8 < have
+                          ? (uint32_t)(cp_row[j] * (int)ldx * 2 + (cp_chunk[j] << 4))
+                          : kOutOfRange;
+            off1[j] = off0[j];
+        }
+    }
+    const uint32_t cp_lds = lds0 + (uint32_t)(GRP == 0 ? 0 : B_BASE) + (uint32_t)q * 1024;
+    auto copy_piece = [&](int c) {
+        if constexpr (LX == LINES) {
+            const int k0 = (c >> 1) * 64, left = w.k - k0;
+            const uint8_t *src = x + (left > 0 ? k0 : 0) * 2;
+            const uint32_t dst = cp_lds + (uint32_t)(c % 5) * kPiece;
+            const bool odd = c & 1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t off = odd ? off1[j] : off0[j];
+                copy16(rsrc_words(src), cp_chunk[j] * 8 < left ? off : kOutOfRange, dst + j * 4096);
+            }
+        } else {
+            const int k0 = c * 32, left = w.k - k0;
+            const uint8_t *src = x + (left > 0 ? k0 * ldx : 0) * 2;
+            const uint32_t dst = cp_lds + (uint32_t)(c & 3) * kPiece;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                copy16(rsrc_words(src), cp_row[j] < left ? off0[j] : kOutOfRange, dst + j * 4096);
+        }
+    };
+
+    // Fragment reads: lane l gets row (or column) l % 32 of a 32-wide block at
+    // k 8 * (l / 32) .. + 7 of a 16-deep step, two steps per half-iteration.
+    const int g4 = lane >> 4, si = lane & 15;
+    const int tr_krow = 8 * (g4 >> 1) + (si >> 2);
+    auto lines_lane = [&](int r0) { return (uint32_t)(r0 * 128) + ((half ^ swz_row(r0)) << 4); };
+    auto krows_lane = [&](int col) {
+        const int n = col + 16 * (g4 & 1) + 4 * (si & 3);
+        return (uint32_t)(tr_krow * 512 + (((n >> 3) ^ (int)swz_krow(tr_krow)) << 4) + (n & 7) * 2);
+    };
+    const uint32_t a_line = lines_lane(l32), b_line = lines_lane((q & 1) * 64 + l32);
+    uint32_t a_tr[4], b_tr[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        a_tr[i] = krows_lane(GRP * 128 + i * 32);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        b_tr[i] = krows_lane(q * 64 + i * 32);
+    // block i (32 rows on: bit 2 of the swizzle flips) of a LINES piece
+    auto read_line = [&](uint32_t piece, uint32_t line, int odd, int st, int i) {
+        const uint32_t xor_bits = (uint32_t)(st << 5) | (uint32_t)((i & 1) << 6);
+        return *(const u32x4 *)(lds + piece + i * 4096 + ((line ^ ((uint32_t)odd << 6)) ^ xor_bits));
+    };
+    auto read_tr = [&](uint32_t piece, uint32_t tr, int st) {
+        const uint8_t *p = lds + piece + tr + st * 16 * 512;
+        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(GSK_LDS_PTR(i16x4, p));
+        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(GSK_LDS_PTR(i16x4, p + 4 * 512));
+        const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
+        return u32x4{l2[0], l2[1], h2[0], h2[1]};
+    };
+    u32x4 fa[2][4], fb[2][2];
+    auto read_frags = [&](int h) {
+        const int even = h & ~1, odd = h & 1;
+        const uint32_t pa = (uint32_t)(LA == LINES ? (even + GRP) % 5 : h & 3) * kPiece;
+        const uint32_t pb = B_BASE + (uint32_t)(LB == LINES ? (even + (q >> 1)) % 5 : h & 3) * kPiece;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                fa[st][i] = LA == LINES ? read_line(pa, a_line, odd, st, i) : read_tr(pa, a_tr[i], st);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                fb[st][i] = LB == LINES ? read_line(pb, b_line, odd, st, i) : read_tr(pb, b_tr[i], st);
+        }
+    };
+    auto multiply = [&]() {
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                mfma16<DT>(acc[i >> 1][i & 1], fb[st][i & 1], fa[st][i >> 1]);
+    };
+    // pieces (of four copies) that may be in flight at the end of a phase
+    constexpr int kInFlight = (GRP == 1 && LB == LINES ? 1 : 2) * 4;
+    auto phase_end = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<kInFlight>();
+        wait_lds();
+        barrier_only();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        acc[i >> 1][i & 1] = f32x16{};
+    const int n = (w.k + 31) / 32;
+    if (n == 0)
+        return;
+    copy_piece(0);
+    copy_piece(1);
+    copy_piece(2);
+    phase_end();
+    if constexpr (GRP == 0) {
+        copy_piece(3);
+        read_frags(0);
+    }
+    phase_end();
+    for (int h = 0; h < n; ++h) {
+        if constexpr (GRP == 0) {
+            multiply();
+            phase_end();
+            if (h + 1 < n) {
+                copy_piece(h + 4);
+                read_frags(h + 1);
+            }
+            phase_end();
+        } else {
+            copy_piece(h + 3);
+            read_frags(h);
+            phase_end();
+            multiply();
+            phase_end();
+        }
+    }
+    wait_vmcnt<0>();  // the zero-filling copies past the end
+}
+
+// The workgroup's tile (c: C at the tile's row 0, column 0 of the matrix; n0:
+// its first column), by both groups.
+template <int DT, int LA, int LB>
+__device__ __forceinline__ void big_tile(const TileWork &w, uint8_t *c, int n0, int N, int c_dtype,
+                                         bool c_vec, uint8_t *lds)
+{
+    // wave index as a scalar: the group branch is uniform
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(c);
+    const bool vec = c_vec || n0 + kBig <= N;
+    const uint32_t row_bytes = (uint32_t)N * (c_dtype ? 2 : 4);
+    f32x16 acc[4][2];
+    auto store = [&](int grp, int q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            store_block(acc[i >> 1][i & 1], rsrc, row_bytes, grp * 128 + (i >> 1) * 32, w.m,
+                        n0 + q * 64 + (i & 1) * 32, N, vec, c_dtype);
+    };
+    // each group has its own copy of everything, so no register value is
+    // merged between the groups' paths
+    if (wave < 4) {
+        big_tile_group<DT, LA, LB, 0>(acc, w, lds, wave);
+        store(0, wave);
+    } else {
+        big_tile_group<DT, LA, LB, 1>(acc, w, lds, wave - 4);
+        store(1, wave - 4);
+    }
+}
+
+template <int DT, int LB>
+__global__ __launch_bounds__(512, 1) void rows_big_kernel(GroupedArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[(ring_of(LINES) + ring_of(LB)) * kPiece];
+    RowTile t;
+    if (!find_row_tile<kBig>(a, blockIdx.x, &t))
+        return;
+    const int n0 = t.tn * kBig;
+    TileWork w;
+    w.a = a.A + (int64_t)t.m0 * a.lda * 2;
+    // (the rows past the last group multiply nothing: depth 0)
+    w.b = a.B + ((t.g < a.groups ? t.g * a.b_stride : 0) + (LB == LINES ? (int64_t)n0 * a.ldb : n0)) * 2;
+    w.lda = a.lda;
+    w.ldb = a.ldb;
+    w.m = t.m_end - t.m0;
+    w.n = a.N - n0;
+    w.k = t.g < a.groups ? a.K : 0;
+    big_tile<DT, LINES, LB>(w, a.C + (int64_t)t.m0 * a.N * (a.c_dtype ? 2 : 4), n0, a.N, a.c_dtype,
+                            a.c_vec, lds);
+}
+
+template <int DT>
+__global__ __launch_bounds__(512, 1) void wgrad_big_kernel(GroupedArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * ring_of(KROWS) * kPiece];
+    const int64_t per = (int64_t)a.tiles_m * a.tiles_n;
+    const int32_t g = (int32_t)(blockIdx.x / per);
+    const int32_t in = (int32_t)(blockIdx.x - g * per);
+    const int m0 = in / a.tiles_n * kBig, n0 = in % a.tiles_n * kBig;
+    int32_t lo, hi;
+    group_rows(a.offsets, g, a.groups, a.rows, &lo, &hi);
+    TileWork w;
+    w.a = a.A + ((int64_t)lo * a.lda + m0) * 2;
+    w.b = a.B + ((int64_t)lo * a.ldb + n0) * 2;
+    w.lda = a.lda;
+    w.ldb = a.ldb;
+    w.m = a.M - m0;
+    w.n = a.N - n0;
+    w.k = hi - lo;
+    big_tile<DT, KROWS, KROWS>(w, a.C + ((int64_t)g * a.M + m0) * a.N * (a.c_dtype ? 2 : 4), n0, a.N,
+                               a.c_dtype, a.c_vec, lds);
+}
+
 int elem_bytes(int dtype)
 {
     return dtype == GEMM_F32 ? 4 : (dtype == GEMM_F16 || dtype == GEMM_BF16 ? 2 : 0);
@@ -233,6 +510,34 @@ int check(const gemm_grouped *p)
     return 0;
 }
 
+// Leading dimensions the kernels read and where repacked operands lie in the
+// workspace.  The 16-bit kernels copy 16-byte words straight into LDS, so an
+// operand whose rows are no whole words is first copied there with its rows
+// padded by zeros.
+struct Layout {
+    int64_t lda, ldb, b_rows, b_cols;
+    bool pack_a, pack_b;
+    size_t off_b, bytes;
+};
+
+size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
+
+Layout layout(const gemm_grouped *p)
+{
+    const int E = elem_bytes(p->dtype);
+    Layout l{};
+    l.b_cols = p->op == GEMM_GROUPED_ROWS_BT ? p->K : p->N;
+    l.b_rows = p->op == GEMM_GROUPED_WGRAD ? p->rows
+               : p->groups * (p->op == GEMM_GROUPED_ROWS_BT ? p->N : p->K);
+    l.pack_a = E == 2 && p->K % 8 != 0;
+    l.pack_b = E == 2 && l.b_cols % 8 != 0;
+    l.lda = l.pack_a ? (p->K + 7) / 8 * 8 : p->K;
+    l.ldb = l.pack_b ? (l.b_cols + 7) / 8 * 8 : l.b_cols;
+    l.off_b = l.pack_a ? align_up((size_t)p->rows * l.lda * E) : 0;
+    l.bytes = l.off_b + (l.pack_b ? align_up((size_t)l.b_rows * l.ldb * E) : 0);
+    return l;
+}
+
 }  // namespace
 }  // namespace gsk
 
@@ -242,8 +547,7 @@ extern "C" {
 
 size_t gemm_grouped_workspace_size(const gemm_grouped *p)
 {
-    (void)p;
-    return 0;
+    return check(p) ? 0 : layout(p).bytes;
 }
 
 int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *A, const void *B,
@@ -251,7 +555,7 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
 {
     if (check(p))
         return -1;
-    const bool wgrad = p->op == GEMM_GROUPED_WGRAD;
+    const bool wgrad = p->op == GEMM_GROUPED_WGRAD, bt = p->op == GEMM_GROUPED_ROWS_BT;
     const int64_t c_rows = wgrad ? p->groups * p->K : p->rows;
     if (c_rows == 0 || p->N == 0)
         return 0;
@@ -262,12 +566,17 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
         set_error("NULL argument");
         return -1;
     }
-    if (((uintptr_t)offsets & 3) || ((uintptr_t)C & (CE - 1)) || ((uintptr_t)A & (E - 1)) ||
-        ((uintptr_t)B & (E - 1))) {
-        set_error("misaligned pointer");
+    if (((uintptr_t)offsets & 3) || ((uintptr_t)C & (CE - 1)) || ((uintptr_t)A & 15) ||
+        ((uintptr_t)B & 15) || ((uintptr_t)workspace & 255)) {
+        set_error("misaligned pointer: A and B take 16 bytes, the workspace 256, offsets and C an "
+                  "element");
         return -1;
     }
-    (void)workspace;
+    const Layout l = layout(p);
+    if (l.bytes && !workspace) {
+        set_error("this product needs %zu bytes of workspace", l.bytes);
+        return -2;
+    }
     GroupedArgs a{};
     a.A = (const uint8_t *)A;
     a.B = (const uint8_t *)B;
@@ -278,47 +587,66 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
     a.N = (int32_t)p->N;
     a.K = (int32_t)p->K;
     a.M = (int32_t)p->K;
-    a.b_stride = p->K * p->N;
-    a.lda = (int32_t)p->K;
-    a.ldb = (int32_t)(p->op == GEMM_GROUPED_ROWS_BT ? p->K : p->N);
+    a.lda = (int32_t)l.lda;
+    a.ldb = (int32_t)l.ldb;
+    a.b_stride = l.ldb * (bt ? p->N : p->K);
     a.c_dtype = c_dtype;
     a.c_vec = p->N % 4 == 0 && ((uintptr_t)C & (4 * CE - 1)) == 0;
     a.xcds = 8;
-    a.tiles_n = (int32_t)((p->N + kXTile - 1) / kXTile);
-    a.tiles_m = (int32_t)((p->K + kXTile - 1) / kXTile);
+    const int tile = E == 4 ? kXTile : kBig, threads = E == 4 ? kXThreads : 512;
+    a.tiles_n = (int32_t)((p->N + tile - 1) / tile);
+    a.tiles_m = (int32_t)((p->K + tile - 1) / tile);
     int64_t tiles;
     if (wgrad) {
         tiles = (int64_t)p->groups * a.tiles_m * a.tiles_n;
     } else {
         // a group's rows, and those past the last group, end inside a tile
         const int64_t ends = p->groups + 1 < p->rows ? p->groups + 1 : p->rows;
-        tiles = (p->rows / kXTile + ends) * a.tiles_n;
+        tiles = (p->rows / tile + ends) * a.tiles_n;
         tiles = (tiles + a.xcds - 1) / a.xcds * a.xcds;
     }
-    if (tiles >= ((int64_t)1 << 32) / kXThreads) {
+    if (tiles >= ((int64_t)1 << 32) / threads) {
         set_error("too many tiles for one launch (%lld)", (long long)tiles);
         return -1;
     }
     const hipStream_t s = (hipStream_t)stream;
-#define GSK_EXACT(T)                                                                             \
-    do {                                                                                         \
-        if (wgrad)                                                                               \
-            hipLaunchKernelGGL((wgrad_exact_kernel<T>), dim3((unsigned)tiles), dim3(kXThreads),  \
-                               0, s, a);                                                         \
-        else if (p->op == GEMM_GROUPED_ROWS_BT)                                                  \
-            hipLaunchKernelGGL((rows_exact_kernel<T, true>), dim3((unsigned)tiles),              \
-                               dim3(kXThreads), 0, s, a);                                        \
-        else                                                                                     \
-            hipLaunchKernelGGL((rows_exact_kernel<T, false>), dim3((unsigned)tiles),             \
-                               dim3(kXThreads), 0, s, a);                                        \
-    } while (0)
-    if (p->dtype == GEMM_F32)
-        GSK_EXACT(float);
-    else if (p->dtype == GEMM_F16)
-        GSK_EXACT(_Float16);
-    else
-        GSK_EXACT(__bf16);
-#undef GSK_EXACT
+    if (reads && (l.pack_a || l.pack_b)) {
+        uint8_t *ws = (uint8_t *)workspace;
+        if (launch_pack_pair(A, ws, l.pack_a ? p->rows : 0, p->K, p->K, l.lda, B, ws + l.off_b,
+                             l.pack_b ? l.b_rows : 0, l.b_cols, l.b_cols, l.ldb, E, s)) {
+            set_error("pack launch failed: %s", hipGetErrorString(hipGetLastError()));
+            return -3;
+        }
+        if (l.pack_a)
+            a.A = ws;
+        if (l.pack_b)
+            a.B = ws + l.off_b;
+    }
+#define GSK_GROUPED(KERNEL, ...)                                                                 \
+    hipLaunchKernelGGL((KERNEL<__VA_ARGS__>), dim3((unsigned)tiles), dim3(threads), 0, s, a)
+    if (E == 4) {
+        if (wgrad)
+            GSK_GROUPED(wgrad_exact_kernel, float);
+        else if (bt)
+            GSK_GROUPED(rows_exact_kernel, float, true);
+        else
+            GSK_GROUPED(rows_exact_kernel, float, false);
+    } else if (p->dtype == GEMM_F16) {
+        if (wgrad)
+            GSK_GROUPED(wgrad_big_kernel, 1);
+        else if (bt)
+            GSK_GROUPED(rows_big_kernel, 1, LINES);
+        else
+            GSK_GROUPED(rows_big_kernel, 1, KROWS);
+    } else {
+        if (wgrad)
+            GSK_GROUPED(wgrad_big_kernel, 2);
+        else if (bt)
+            GSK_GROUPED(rows_big_kernel, 2, LINES);
+        else
+            GSK_GROUPED(rows_big_kernel, 2, KROWS);
+    }
+#undef GSK_GROUPED
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) {
         set_error("grouped product launch failed: %s", hipGetErrorString(e));

@@ -201,6 +201,12 @@ def combine_rows_backward(dy, ys, weights, routing):
     return dys, dweights
 
 
+def _dense(t):
+    """t, contiguous and 16-byte aligned (a view may start anywhere)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _offsets(what, offsets, groups=None):
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or \
             (groups is not None and offsets.numel() != groups + 1):
@@ -235,12 +241,12 @@ def grouped_matmul(a, b, offsets, out_dtype=None):
     _code(a, "a")
     offsets = _offsets("grouped_matmul", offsets, b.shape[0])
     c_type, flags = _c_flags(a.dtype, out_dtype)
-    a = a.contiguous()
+    a = _dense(a)
     op, bt = GROUPED_ROWS, b.transpose(1, 2)
     if not b.is_contiguous() and bt.is_contiguous():
-        op, b = GROUPED_ROWS_BT, bt
+        op, b = GROUPED_ROWS_BT, _dense(bt)
     else:
-        b = b.contiguous()
+        b = _dense(b)
     K, N = bt.shape[2], bt.shape[1]
     c = torch.empty((a.shape[0], N), dtype=c_type, device=dev)
     return _grouped(dev, op, a, b, c, offsets, K, N, b.shape[0], flags)
@@ -258,7 +264,7 @@ def grouped_matmul_wgrad(a, dc, offsets, out_dtype=None):
     _code(a, "a")
     offsets = _offsets("grouped_matmul_wgrad", offsets)
     c_type, flags = _c_flags(a.dtype, out_dtype)
-    a, dc = a.contiguous(), dc.contiguous()
+    a, dc = _dense(a), _dense(dc)
     groups, K, N = offsets.numel() - 1, a.shape[1], dc.shape[1]
     c = torch.empty((groups, K, N), dtype=c_type, device=dev)
     return _grouped(dev, GROUPED_WGRAD, a, dc, c, offsets, K, N, groups, flags)

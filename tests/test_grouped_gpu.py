@@ -155,19 +155,21 @@ def test_not_finite_values_stay_in_their_rows_and_groups(dtype):
 
 
 def test_offsets_out_of_range_or_order_touch_nothing_else():
-    # the buffer may hold anything: the run ends, and rows of sane groups hold
+    # the buffer may hold anything and the run still ends; offsets that
+    # descend make groups overlap, whose rows are then anyone's, and offsets
+    # past the rows end with them
     K, N = 72, 136
     a, b = normal((200, K), "bf16", 1), normal((4, K, N), "bf16", 2)
-    for off in ([0, 50, 10 ** 9, -5, 200], [150, 20, 60, 10, 5], [-9, -1, 2 ** 31 - 1, 2 ** 31 - 1, 0]):
+    for off in ([0, 50, 10 ** 9, -5, 200], [150, 20, 60, 10, 5], [-9, -1, 2 ** 31 - 1, 2 ** 31 - 1, 0],
+                [-3, 50, 10 ** 9, 10 ** 9, 2 ** 31 - 1]):
         o = torch.tensor(off, dtype=torch.int64).to(torch.int32).cuda()
         c = gsk.grouped_matmul(a.cuda(), b.cuda(), o)
         assert c.shape == (200, N)
         w = gsk.grouped_matmul_wgrad(a.cuda(), normal((200, N), "bf16", 3).cuda(), o)
         assert w.shape == (4, K, N)
         torch.cuda.synchronize()
-        if off[0] == 0:
-            ref, size = grouped_ref(f64(a)[:50], f64(b), np.array([0, 50, 50, 50, 50]))
-            within(c[:50], ref, 2 * K * U * size)
+    ref, size = grouped_ref(f64(a), f64(b), np.array([0, 50, 200, 200, 200]))
+    within(c, ref, 2 * K * U * size)
 
 
 def test_strided_inputs_are_taken_as_they_are():
