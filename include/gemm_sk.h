@@ -495,6 +495,37 @@ int gemm_grouped_run(const gemm_grouped *problem, const int32_t *offsets, const 
 /* Bytes of workspace gemm_grouped_run needs (0: none). */
 size_t gemm_grouped_workspace_size(const gemm_grouped *problem);
 
+/* Low-rank adapters of many requests beside a shared projection:
+ *   Y[t] = X[t] . W + scales[a] * (X[t] . A[a]^T) . B[a]^T,  a = ids[t],
+ * and Y[t] = X[t] . W for a row whose id lies outside [0, adapters).  X is rows
+ * x K; W is K x N, or N x K with w_transposed (linear-layer weights); A is
+ * adapters x rank x K and B adapters x N x rank (the weights of the two small
+ * linear layers; adapters of a lower rank are padded with zeros); scales (fp32,
+ * per adapter) may be NULL: all 1.  Y is rows x N, fp32 or, with
+ * GEMM_FLAG_C_INPUT_DTYPE (the only flag), the input dtype.  All arrays are
+ * dense; dtype fp32, fp16 or bf16 with fp32 accumulation; the rank-sized
+ * intermediate keeps at least 16 bits (22 for fp16, 24 for fp32 results).
+ * Rows may be in any order.  An adapter's values, infinities and NaN among
+ * them, reach no row but those that name it.  rows < 2^24, K and N < 2^20,
+ * 1 <= rank <= 128.  A serving call: it has no gradient. */
+typedef struct {
+    int32_t dtype;        /* gemm_dtype of X, W, A and B */
+    int32_t rank;
+    int64_t rows, K, N;
+    int32_t adapters;
+    int32_t w_transposed; /* 0: W is K x N, 1: N x K */
+    uint32_t flags;
+} gemm_adapter;
+
+/* Enqueue it.  X and W are 16-byte aligned, the workspace 256-byte aligned (no
+ * clearing needed; it is used by this call alone while it runs). */
+int gemm_adapter_run(const gemm_adapter *problem, const void *X, const void *W, const void *A,
+                     const void *B, const int32_t *ids, const float *scales, void *Y,
+                     void *workspace, void *stream);
+
+/* Bytes of workspace gemm_adapter_run needs. */
+size_t gemm_adapter_workspace_size(const gemm_adapter *problem);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,7 +13,8 @@ from ._lib import (BF16, DP, DTYPES, F16, F32, I8, FLAG_C_INPUT_DTYPE,
 from .plan import FixupError, GemmPlan, matmul, plan_for_device
 
 _ROWS = ("Routing", "route_rows", "gather_rows", "gather_rows_backward", "combine_rows",
-         "combine_rows_backward", "grouped_matmul", "grouped_matmul_wgrad")
+         "combine_rows_backward", "grouped_matmul", "grouped_matmul_wgrad",
+         "adapter_matmul")
 
 
 def __getattr__(name):

@@ -9,7 +9,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemmsk.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("kernels.hip", "api.hip", "routing.hip",
-                                           "grouped.hip")]
+                                           "grouped.hip", "adapter.hip")]
 ARCH = "gfx950"
 
 

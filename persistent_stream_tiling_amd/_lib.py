@@ -83,6 +83,12 @@ class Grouped(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+class Adapter(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("rank", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("adapters", ctypes.c_int32),
+                ("w_transposed", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
 EXPORTS = ("gemm_plan_create", "gemm_plan_create_for_device", "gemm_run", "gemm_run_noalloc",
            "gemm_plan_destroy",
            "gemm_plan_workspace_size", "gemm_plan_describe", "gemm_last_error",
@@ -90,7 +96,7 @@ EXPORTS = ("gemm_plan_create", "gemm_plan_create_for_device", "gemm_run", "gemm_
            "gemm_plan_logical_wg", "gemm_workspace_status", "gemm_variant_count",
            "gemm_variant_get", "gemm_route", "gemm_route_workspace_size", "gemm_gather_rows",
            "gemm_combine_rows", "gemm_combine_rows_backward", "gemm_grouped_run",
-           "gemm_grouped_workspace_size")
+           "gemm_grouped_workspace_size", "gemm_adapter_run", "gemm_adapter_workspace_size")
 
 _lib = None
 
@@ -153,6 +159,10 @@ def load(path=None):
     lib.gemm_grouped_run.restype = ctypes.c_int
     lib.gemm_grouped_workspace_size.argtypes = [ctypes.POINTER(Grouped)]
     lib.gemm_grouped_workspace_size.restype = ctypes.c_size_t
+    lib.gemm_adapter_run.argtypes = [ctypes.POINTER(Adapter), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.gemm_adapter_run.restype = ctypes.c_int
+    lib.gemm_adapter_workspace_size.argtypes = [ctypes.POINTER(Adapter)]
+    lib.gemm_adapter_workspace_size.restype = ctypes.c_size_t
     _lib = lib
     return lib
 

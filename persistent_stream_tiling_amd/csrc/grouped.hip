@@ -6,153 +6,17 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include "device.h"
 #include "errors.h"
 #include "gemm_sk.h"
 #include "grouped.h"
 #include "kernels.h"
+#include "tiles.h"
 
 namespace gsk {
 
 using namespace dev;
 
 namespace {
-
-// ---------------------------------------------------------------------------
-// fp32: the fp32 matrix instruction, 128x128 tiles, any sizes and alignments.
-//
-// An operand is a slab of 128 rows (m or n) by 16 k per iteration.  It lies in
-// memory either with k contiguous (KC: 8 consecutive k per thread) or with
-// m / n contiguous (8 consecutive m per thread), and in LDS always as
-// [k][m], the order the 32x32x2 instruction reads (lane l: row l % 32, k = l /
-// 32).  LDS rows are 160 floats apart: the two k rows that one read touches
-// are then 32 banks apart.  Two LDS buffers; the next slab's loads are in
-// flight while the current one is multiplied.
-constexpr int kXTile = 128, kXDeep = 16, kXThreads = 256, kXPitch = 160;
-
-template <typename T>
-struct Packed8 {
-    struct __attribute__((packed, aligned(sizeof(T)))) Words {
-        uint32_t w[8 * sizeof(T) / 4];
-    };
-};
-
-// Eight consecutive elements at p, of which the first n (0 .. 8) exist.
-template <typename T>
-__device__ __forceinline__ void load8(float (&x)[8], const T *p, int n)
-{
-    T t[8];
-    if (n >= 8) {
-        const auto w = *(const typename Packed8<T>::Words *)p;
-        __builtin_memcpy(t, &w, sizeof(t));
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            t[e] = e < n ? p[e] : (T)0.0f;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        x[e] = (float)t[e];
-}
-
-// One thread's share of a slab: rows [0, rows) x k [0, k) exist at p.
-template <typename T, bool KC>
-__device__ __forceinline__ void load_slab(float (&x)[8], const T *p, int64_t ld, int rows, int k)
-{
-    const int tid = threadIdx.x;
-    const int r = KC ? tid >> 1 : (tid & 15) * 8, kk = KC ? (tid & 1) * 8 : tid >> 4;
-    const int n = KC ? (r < rows ? k - kk : 0) : (kk < k ? rows - r : 0);
-    load8(x, KC ? p + r * ld + kk : p + kk * ld + r, n);
-}
-
-template <bool KC>
-__device__ __forceinline__ void park_slab(float *lds, const float (&x)[8])
-{
-    const int tid = threadIdx.x;
-    if constexpr (KC) {
-        const int r = tid >> 1, kk = (tid & 1) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            lds[(kk + e) * kXPitch + r] = x[e];
-    } else {
-        float *p = lds + (tid >> 4) * kXPitch + (tid & 15) * 8;
-        *(f32x4 *)p = f32x4{x[0], x[1], x[2], x[3]};
-        *(f32x4 *)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
-    }
-}
-
-// acc (2 x 2 blocks of 32x32 per wave, 2 x 2 waves) = the tile's sums over k
-// in [0, k).  The operands are swapped in the instruction, so lane l holds
-// C[32*mt + l % 32][32*nt + 8*g + 4*(l / 32) + e] in register 4*g + e.
-template <typename T, bool A_KC, bool B_KC>
-__device__ __forceinline__ void exact_tile(f32x16 (&acc)[2][2], float *lds, const T *a, int64_t lda,
-                                           int m, const T *b, int64_t ldb, int n, int k)
-{
-    constexpr int kSlab = kXDeep * kXPitch;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int half = lane >> 5, l32 = lane & 31;
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-    const int64_t a_step = A_KC ? kXDeep : kXDeep * lda, b_step = B_KC ? kXDeep : kXDeep * ldb;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        acc[i >> 1][i & 1] = f32x16{};
-    float xa[8], xb[8];
-    if (k > 0) {
-        load_slab<T, A_KC>(xa, a, lda, m, k);
-        load_slab<T, B_KC>(xb, b, ldb, n, k);
-    }
-    for (int k0 = 0, buf = 0; k0 < k; k0 += kXDeep, buf ^= 1) {
-        float *sa = lds + buf * 2 * kSlab, *sb = sa + kSlab;
-        park_slab<A_KC>(sa, xa);
-        park_slab<B_KC>(sb, xb);
-        // one barrier per slab: a wave two slabs on would overwrite this
-        // buffer, and to get there it has to pass the next barrier
-        __syncthreads();
-        if (k0 + kXDeep < k) {
-            a += a_step;
-            b += b_step;
-            load_slab<T, A_KC>(xa, a, lda, m, k - k0 - kXDeep);
-            load_slab<T, B_KC>(xb, b, ldb, n, k - k0 - kXDeep);
-        }
-#pragma unroll
-        for (int kk = 0; kk < kXDeep; kk += 2) {
-            const int row = (kk + half) * kXPitch + l32;
-            float fa[2], fb[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                fa[i] = sa[row + wm + 32 * i];
-                fb[i] = sb[row + wn + 32 * i];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[i >> 1][i & 1] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[i & 1], fa[i >> 1],
-                                                                          acc[i >> 1][i & 1], 0, 0, 0);
-        }
-    }
-}
-
-// Rows m0 .. and columns n0 .. of the tile to C, whose row m0 starts at c.
-__device__ __forceinline__ void store_exact(const f32x16 (&acc)[2][2], uint8_t *c, int64_t ldc,
-                                            int m, int n0, int N, int c_dtype, bool c_vec)
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int half = lane >> 5, l32 = lane & 31;
-    const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(c);
-    const bool vec = c_vec || n0 + kXTile <= N;
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-        const int row = (wave >> 1) * 64 + 32 * mt + l32;
-        const uint32_t row_off = (uint32_t)(row * ldc * (c_dtype ? 2 : 4));
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                store_four(f32x4{acc[mt][nt][4 * g], acc[mt][nt][4 * g + 1], acc[mt][nt][4 * g + 2],
-                                 acc[mt][nt][4 * g + 3]},
-                           rsrc, row_off, n0 + (wave & 1) * 64 + 32 * nt + 8 * g + 4 * half, N,
-                           row < m, vec, c_dtype);
-    }
-}
 
 template <typename T, bool B_KC>
 __global__ __launch_bounds__(kXThreads) void rows_exact_kernel(GroupedArgs a)
@@ -189,238 +53,31 @@ __global__ __launch_bounds__(kXThreads) void wgrad_exact_kernel(GroupedArgs a)
                 a.N, a.c_dtype, a.c_vec);
 }
 
-// ---------------------------------------------------------------------------
-// fp16 / bf16, 256x256 tiles, eight waves in two groups that take turns.
-//
-// Group 0 (waves 0-3) computes tile rows 0-127, group 1 (waves 4-7) rows
-// 128-255, each wave a 128 x 64 block; wave q of both groups runs on the same
-// SIMD.  Time is cut into phases between workgroup barriers.  With
-// half-iterations h (32 k each):
-//   phase 2h:     group 0 multiplies h (16 MFMAs, operands in registers);
-//                 group 1 copies its operand's piece h + 3 and reads h;
-//   phase 2h + 1: group 1 multiplies h;
-//                 group 0 copies its operand's piece h + 4 and reads h + 1
-// (group 0 reads h = 0 in a phase of its own before phase 0).  Group 0 copies
-// operand A, group 1 operand B, straight from global memory into LDS, in
-// pieces of 16 KiB: four 1 KiB copies per wave.
-//
-// An operand lies in memory in one of two ways, and its pieces with it:
-//   LINES   k contiguous.  Piece c holds 128 of the tile's 256 rows (those of
-//           parity c & 1) by the 64 k of iteration c >> 1, in whole 128-byte
-//           lines; fragments are 16-byte reads.  Ring of 5 pieces.
-//   KROWS   m or n contiguous.  Piece c holds the 32 k-rows of half-iteration
-//           c by all 256 columns; fragments are transposing reads.  Ring of 4.
-// So the product with B as it lies (A LINES, B KROWS), with B transposed
-// (LINES, LINES) and the weight gradient (KROWS, KROWS) are one kernel, none
-// with a transposing pass over memory, in at most 160 KiB of LDS.
-//
-// Why the rings are long enough.  Every phase ends with a wait for the
-// wave's own copies (at most two pieces' in flight; one for B in LINES), for
-// the LDS reads it issued, and a barrier.  Copied by group 0, piece c is issued
-// in phase 2c - 7 and landed by the end of 2c - 3; by group 1, in 2c - 6,
-// landed by the end of 2c - 2 (2c - 4 with one in flight).  First reads:
-//   A LINES  even pieces by group 0 in phase 2c - 1, odd by group 1 in 2c - 2
-//   A KROWS  2c - 1          B KROWS  2c - 1
-//   B LINES  odd pieces by group 0 in 2c - 3, even in 2c - 1
-// and the piece that c overwrites was last read in
-//   A LINES  2c - 9 (even; c - 5)   or 2c - 10 (odd)
-//   A KROWS  2c - 8 (c - 4)         B KROWS  2c - 8 (c - 4)
-//   B LINES  2c - 8 (c - 5, even)   or 2c - 10 (odd)
-// each before the copy's phase.  Copies past the end of k read nothing
-// (out-of-range offsets) and zero a free piece, so the wait counts are
-// constants.
-enum { LINES = 0, KROWS = 1 };
-
-constexpr int kBig = 256, kPiece = 16384;
-
-constexpr int ring_of(int layout) { return layout == LINES ? 5 : 4; }
-
-// What one workgroup multiplies: the tile's corner in both operands.
-struct TileWork {
-    const uint8_t *a, *b;  // LINES: row 0, k 0.  KROWS: k-row 0, column 0
-    int64_t lda, ldb;      // elements
-    int m, n, k;           // rows and columns that exist from the corner on; depth
-};
-
-template <int DT, int LA, int LB, int GRP>
-__device__ __forceinline__ void big_tile_group(f32x16 (&acc)[4][2], const TileWork &w, uint8_t *lds,
-                                               int q)
+__device__ __forceinline__ uint32_t c_row_bytes(const GroupedArgs &a)
 {
-    constexpr int LX = GRP == 0 ? LA : LB;  // layout of the operand this group copies
-    constexpr int RA = ring_of(LA), RB = ring_of(LB);
-    constexpr int B_BASE = RA * kPiece;
-    const int lane = threadIdx.x & 63;
-    const int half = lane >> 5, l32 = lane & 31;
-    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
-
-    // Copies: copy j of this wave fills KiB 4j + q of a piece.
-    const uint8_t *x = GRP == 0 ? w.a : w.b;
-    const int64_t ldx = GRP == 0 ? w.lda : w.ldb;
-    const int have = GRP == 0 ? w.m : w.n;  // rows (LINES) or columns (KROWS) that exist
-    int cp_row[4], cp_chunk[4];
-    uint32_t off0[4], off1[4];  // LINES: even and odd pieces
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if constexpr (LX == LINES) {
-            cp_row[j] = 8 * (4 * j + q) + (lane >> 3);
-            cp_chunk[j] = (lane & 7) ^ (int)swz_row(cp_row[j]);
-            const uint32_t o = (uint32_t)(cp_row[j] * (int)ldx * 2 + (cp_chunk[j] << 4));
-            off0[j] = cp_row[j] < have ? o : kOutOfRange;
-            off1[j] = cp_row[j] + 128 < have ? o + (uint32_t)(256 * (int)ldx) : kOutOfRange;
-        } else {
-            cp_row[j] = 2 * (4 * j + q) + (lane >> 5);
-            cp_chunk[j] = (lane & 31) ^ (int)swz_krow(cp_row[j]);
-            off0[j] = cp_chunk[j] * 8 < have
-                          ? (uint32_t)(cp_row[j] * (int)ldx * 2 + (cp_chunk[j] << 4))
-                          : kOutOfRange;
-            off1[j] = off0[j];
-        }
-    }
-    const uint32_t cp_lds = lds0 + (uint32_t)(GRP == 0 ? 0 : B_BASE) + (uint32_t)q * 1024;
-    auto copy_piece = [&](int c) {
-        if constexpr (LX == LINES) {
-            const int k0 = (c >> 1) * 64, left = w.k - k0;
-            const uint8_t *src = x + (left > 0 ? k0 : 0) * 2;
-            const uint32_t dst = cp_lds + (uint32_t)(c % 5) * kPiece;
-            const bool odd = c & 1;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t off = odd ? off1[j] : off0[j];
-                copy16(rsrc_words(src), cp_chunk[j] * 8 < left ? off : kOutOfRange, dst + j * 4096);
-            }
-        } else {
-            const int k0 = c * 32, left = w.k - k0;
-            const uint8_t *src = x + (left > 0 ? k0 * ldx : 0) * 2;
-            const uint32_t dst = cp_lds + (uint32_t)(c & 3) * kPiece;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                copy16(rsrc_words(src), cp_row[j] < left ? off0[j] : kOutOfRange, dst + j * 4096);
-        }
-    };
-
-    // Fragment reads: lane l gets row (or column) l % 32 of a 32-wide block at
-    // k 8 * (l / 32) .. + 7 of a 16-deep step, two steps per half-iteration.
-    const int g4 = lane >> 4, si = lane & 15;
-    const int tr_krow = 8 * (g4 >> 1) + (si >> 2);
-    auto lines_lane = [&](int r0) { return (uint32_t)(r0 * 128) + ((half ^ swz_row(r0)) << 4); };
-    auto krows_lane = [&](int col) {
-        const int n = col + 16 * (g4 & 1) + 4 * (si & 3);
-        return (uint32_t)(tr_krow * 512 + (((n >> 3) ^ (int)swz_krow(tr_krow)) << 4) + (n & 7) * 2);
-    };
-    const uint32_t a_line = lines_lane(l32), b_line = lines_lane((q & 1) * 64 + l32);
-    uint32_t a_tr[4], b_tr[2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        a_tr[i] = krows_lane(GRP * 128 + i * 32);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        b_tr[i] = krows_lane(q * 64 + i * 32);
-    // block i (32 rows on: bit 2 of the swizzle flips) of a LINES piece
-    auto read_line = [&](uint32_t piece, uint32_t line, int odd, int st, int i) {
-        const uint32_t xor_bits = (uint32_t)(st << 5) | (uint32_t)((i & 1) << 6);
-        return *(const u32x4 *)(lds + piece + i * 4096 + ((line ^ ((uint32_t)odd << 6)) ^ xor_bits));
-    };
-    auto read_tr = [&](uint32_t piece, uint32_t tr, int st) {
-        const uint8_t *p = lds + piece + tr + st * 16 * 512;
-        const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(GSK_LDS_PTR(i16x4, p));
-        const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(GSK_LDS_PTR(i16x4, p + 4 * 512));
-        const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
-        return u32x4{l2[0], l2[1], h2[0], h2[1]};
-    };
-    u32x4 fa[2][4], fb[2][2];
-    auto read_frags = [&](int h) {
-        const int even = h & ~1, odd = h & 1;
-        const uint32_t pa = (uint32_t)(LA == LINES ? (even + GRP) % 5 : h & 3) * kPiece;
-        const uint32_t pb = B_BASE + (uint32_t)(LB == LINES ? (even + (q >> 1)) % 5 : h & 3) * kPiece;
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                fa[st][i] = LA == LINES ? read_line(pa, a_line, odd, st, i) : read_tr(pa, a_tr[i], st);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                fb[st][i] = LB == LINES ? read_line(pb, b_line, odd, st, i) : read_tr(pb, b_tr[i], st);
-        }
-    };
-    auto multiply = [&]() {
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                mfma16<DT>(acc[i >> 1][i & 1], fb[st][i & 1], fa[st][i >> 1]);
-    };
-    // pieces (of four copies) that may be in flight at the end of a phase
-    constexpr int kInFlight = (GRP == 1 && LB == LINES ? 1 : 2) * 4;
-    auto phase_end = [&]() {
-        __builtin_amdgcn_sched_barrier(0);
-        wait_vmcnt<kInFlight>();
-        wait_lds();
-        barrier_only();
-        __builtin_amdgcn_sched_barrier(0);
-    };
-
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        acc[i >> 1][i & 1] = f32x16{};
-    const int n = (w.k + 31) / 32;
-    if (n == 0)
-        return;
-    copy_piece(0);
-    copy_piece(1);
-    copy_piece(2);
-    phase_end();
-    if constexpr (GRP == 0) {
-        copy_piece(3);
-        read_frags(0);
-    }
-    phase_end();
-    for (int h = 0; h < n; ++h) {
-        if constexpr (GRP == 0) {
-            multiply();
-            phase_end();
-            if (h + 1 < n) {
-                copy_piece(h + 4);
-                read_frags(h + 1);
-            }
-            phase_end();
-        } else {
-            copy_piece(h + 3);
-            read_frags(h);
-            phase_end();
-            multiply();
-            phase_end();
-        }
-    }
-    wait_vmcnt<0>();  // the zero-filling copies past the end
+    return (uint32_t)a.N * (a.c_dtype ? 2 : 4);
 }
 
-// The workgroup's tile (c: C at the tile's row 0, column 0 of the matrix; n0:
-// its first column), by both groups.
-template <int DT, int LA, int LB>
-__device__ __forceinline__ void big_tile(const TileWork &w, uint8_t *c, int n0, int N, int c_dtype,
-                                         bool c_vec, uint8_t *lds)
+// Descriptor for the rows of C from `row` on.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t c_rows(const GroupedArgs &a, int64_t row)
 {
-    // wave index as a scalar: the group branch is uniform
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(c);
-    const bool vec = c_vec || n0 + kBig <= N;
-    const uint32_t row_bytes = (uint32_t)N * (c_dtype ? 2 : 4);
-    f32x16 acc[4][2];
-    auto store = [&](int grp, int q) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            store_block(acc[i >> 1][i & 1], rsrc, row_bytes, grp * 128 + (i >> 1) * 32, w.m,
-                        n0 + q * 64 + (i & 1) * 32, N, vec, c_dtype);
-    };
-    // each group has its own copy of everything, so no register value is
-    // merged between the groups' paths
-    if (wave < 4) {
-        big_tile_group<DT, LA, LB, 0>(acc, w, lds, wave);
-        store(0, wave);
-    } else {
-        big_tile_group<DT, LA, LB, 1>(acc, w, lds, wave - 4);
-        store(1, wave - 4);
-    }
+    return make_rsrc(a.C + row * c_row_bytes(a));
+}
+
+// Row tile t by the columns from n0 on.  The rows past the last group
+// multiply nothing: depth 0.
+template <int LB>
+__device__ __forceinline__ TileWork rows_work(const GroupedArgs &a, const RowTile &t, int n0)
+{
+    TileWork w;
+    w.a = a.A + (int64_t)t.m0 * a.lda * 2;
+    w.b = a.B + ((t.g < a.groups ? t.g * a.b_stride : 0) + (LB == LINES ? (int64_t)n0 * a.ldb : n0)) * 2;
+    w.lda = a.lda;
+    w.ldb = a.ldb;
+    w.m = t.m_end - t.m0;
+    w.n = a.N - n0;
+    w.k = t.g < a.groups ? a.K : 0;
+    return w;
 }
 
 template <int DT, int LB>
@@ -431,17 +88,34 @@ __global__ __launch_bounds__(512, 1) void rows_big_kernel(GroupedArgs a)
     if (!find_row_tile<kBig>(a, blockIdx.x, &t))
         return;
     const int n0 = t.tn * kBig;
-    TileWork w;
-    w.a = a.A + (int64_t)t.m0 * a.lda * 2;
-    // (the rows past the last group multiply nothing: depth 0)
-    w.b = a.B + ((t.g < a.groups ? t.g * a.b_stride : 0) + (LB == LINES ? (int64_t)n0 * a.ldb : n0)) * 2;
-    w.lda = a.lda;
-    w.ldb = a.ldb;
-    w.m = t.m_end - t.m0;
-    w.n = a.N - n0;
-    w.k = t.g < a.groups ? a.K : 0;
-    big_tile<DT, LINES, LB>(w, a.C + (int64_t)t.m0 * a.N * (a.c_dtype ? 2 : 4), n0, a.N, a.c_dtype,
-                            a.c_vec, lds);
+    const TileWork w = rows_work<LB>(a, t, n0);
+    const __amdgpu_buffer_rsrc_t c = c_rows(a, t.m0);
+    const bool vec = a.c_vec || n0 + kBig <= a.N;
+    big_tile<DT, LINES, LB>(w, lds, [&](const f32x16 (&acc)[4][2], int row, int col) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            store_block(acc[i >> 1][i & 1], c, c_row_bytes(a), row + (i >> 1) * 32, w.m,
+                        n0 + col + (i & 1) * 32, a.N, vec, a.c_dtype);
+    });
+}
+
+template <int DT, int LB, int MT>
+__global__ __launch_bounds__(256, 2) void rows_narrow_kernel(GroupedArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[narrow_lds(MT)];
+    RowTile t;
+    if (!find_row_tile<32 * MT>(a, blockIdx.x, &t))
+        return;
+    const int n0 = t.tn * kNarrow;
+    const TileWork w = rows_work<LB>(a, t, n0);
+    f32x16 acc[MT][1];
+    narrow_tile<DT, LB, MT>(acc, w, lds);
+    const __amdgpu_buffer_rsrc_t c = c_rows(a, t.m0);
+    const bool vec = a.c_vec || n0 + kNarrow <= a.N;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        store_block(acc[i][0], c, c_row_bytes(a), i * 32, w.m, n0 + wave * 32, a.N, vec, a.c_dtype);
 }
 
 template <int DT>
@@ -462,8 +136,14 @@ __global__ __launch_bounds__(512, 1) void wgrad_big_kernel(GroupedArgs a)
     w.m = a.M - m0;
     w.n = a.N - n0;
     w.k = hi - lo;
-    big_tile<DT, KROWS, KROWS>(w, a.C + ((int64_t)g * a.M + m0) * a.N * (a.c_dtype ? 2 : 4), n0, a.N,
-                               a.c_dtype, a.c_vec, lds);
+    const __amdgpu_buffer_rsrc_t c = c_rows(a, (int64_t)g * a.M + m0);
+    const bool vec = a.c_vec || n0 + kBig <= a.N;
+    big_tile<DT, KROWS, KROWS>(w, lds, [&](const f32x16 (&acc)[4][2], int row, int col) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            store_block(acc[i >> 1][i & 1], c, c_row_bytes(a), row + (i >> 1) * 32, w.m,
+                        n0 + col + (i & 1) * 32, a.N, vec, a.c_dtype);
+    });
 }
 
 int elem_bytes(int dtype)
@@ -520,6 +200,23 @@ struct Layout {
     size_t off_b, bytes;
 };
 
+// Row blocks of 32 per tile of the few-rows kernel, 0 for 256x256 tiles, by
+// the mean rows per group.  Tiles much taller than a group multiply zeros;
+// lower ones read the group's matrix again.  Measured at 128 groups x 2048 x
+// 1536 bf16 with MT = 1 / 2 / 4 / 256x256 tiles (us): mean 4 rows 141 / 140 /
+// 143 / 157, 32 rows 180 / 157 / 155 / 163, 64 rows 233 / 199 / 167 / 173, 128
+// rows 363 / 257 / 228 / 198; at 8 groups x 4096 x 4096 (128 tiles of 256x256,
+// half the CUs): 4 rows 42 / 42 / 52 / 84, 64 rows 109 / 71 / 60 / 85, 192 rows
+// 251 / 141 / 75 / 89, 256 rows 324 / 180 / 127 / 97.
+int narrow_mt(const gemm_grouped *p)
+{
+    const int64_t mean = p->rows / p->groups;
+    const int64_t big_tiles = p->groups * ((p->N + kBig - 1) / kBig);
+    if (mean >= 224 || (mean >= 112 && big_tiles >= 512))
+        return 0;
+    return mean <= 8 ? 1 : (mean <= 48 ? 2 : 4);
+}
+
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
 Layout layout(const gemm_grouped *p)
@@ -573,10 +270,6 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
         return -1;
     }
     const Layout l = layout(p);
-    if (l.bytes && !workspace) {
-        set_error("this product needs %zu bytes of workspace", l.bytes);
-        return -2;
-    }
     GroupedArgs a{};
     a.A = (const uint8_t *)A;
     a.B = (const uint8_t *)B;
@@ -593,21 +286,28 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
     a.c_dtype = c_dtype;
     a.c_vec = p->N % 4 == 0 && ((uintptr_t)C & (4 * CE - 1)) == 0;
     a.xcds = 8;
-    const int tile = E == 4 ? kXTile : kBig, threads = E == 4 ? kXThreads : 512;
-    a.tiles_n = (int32_t)((p->N + tile - 1) / tile);
-    a.tiles_m = (int32_t)((p->K + tile - 1) / tile);
+    const int mt = E == 4 || wgrad ? 0 : narrow_mt(p);
+    const int bm = E == 4 ? kXTile : (mt ? 32 * mt : kBig);
+    const int bn = E == 4 ? kXTile : (mt ? kNarrow : kBig);
+    const int threads = E == 4 || mt ? 256 : 512;
+    a.tiles_n = (int32_t)((p->N + bn - 1) / bn);
+    a.tiles_m = (int32_t)((p->K + bm - 1) / bm);
     int64_t tiles;
     if (wgrad) {
         tiles = (int64_t)p->groups * a.tiles_m * a.tiles_n;
     } else {
         // a group's rows, and those past the last group, end inside a tile
         const int64_t ends = p->groups + 1 < p->rows ? p->groups + 1 : p->rows;
-        tiles = (p->rows / tile + ends) * a.tiles_n;
+        tiles = (p->rows / bm + ends) * a.tiles_n;
         tiles = (tiles + a.xcds - 1) / a.xcds * a.xcds;
     }
     if (tiles >= ((int64_t)1 << 32) / threads) {
         set_error("too many tiles for one launch (%lld)", (long long)tiles);
         return -1;
+    }
+    if (l.bytes && !workspace) {
+        set_error("this product needs %zu bytes of workspace", l.bytes);
+        return -2;
     }
     const hipStream_t s = (hipStream_t)stream;
     if (reads && (l.pack_a || l.pack_b)) {
@@ -624,6 +324,27 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
     }
 #define GSK_GROUPED(KERNEL, ...)                                                                 \
     hipLaunchKernelGGL((KERNEL<__VA_ARGS__>), dim3((unsigned)tiles), dim3(threads), 0, s, a)
+#define GSK_GROUPED_16(DT)                                                                       \
+    do {                                                                                         \
+        if (wgrad)                                                                               \
+            GSK_GROUPED(wgrad_big_kernel, DT);                                                   \
+        else if (mt == 1 && bt)                                                                  \
+            GSK_GROUPED(rows_narrow_kernel, DT, LINES, 1);                                       \
+        else if (mt == 1)                                                                        \
+            GSK_GROUPED(rows_narrow_kernel, DT, KROWS, 1);                                       \
+        else if (mt == 2 && bt)                                                                  \
+            GSK_GROUPED(rows_narrow_kernel, DT, LINES, 2);                                       \
+        else if (mt == 2)                                                                        \
+            GSK_GROUPED(rows_narrow_kernel, DT, KROWS, 2);                                       \
+        else if (mt == 4 && bt)                                                                  \
+            GSK_GROUPED(rows_narrow_kernel, DT, LINES, 4);                                       \
+        else if (mt == 4)                                                                        \
+            GSK_GROUPED(rows_narrow_kernel, DT, KROWS, 4);                                       \
+        else if (bt)                                                                             \
+            GSK_GROUPED(rows_big_kernel, DT, LINES);                                             \
+        else                                                                                     \
+            GSK_GROUPED(rows_big_kernel, DT, KROWS);                                             \
+    } while (0)
     if (E == 4) {
         if (wgrad)
             GSK_GROUPED(wgrad_exact_kernel, float);
@@ -632,20 +353,11 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
         else
             GSK_GROUPED(rows_exact_kernel, float, false);
     } else if (p->dtype == GEMM_F16) {
-        if (wgrad)
-            GSK_GROUPED(wgrad_big_kernel, 1);
-        else if (bt)
-            GSK_GROUPED(rows_big_kernel, 1, LINES);
-        else
-            GSK_GROUPED(rows_big_kernel, 1, KROWS);
+        GSK_GROUPED_16(1);
     } else {
-        if (wgrad)
-            GSK_GROUPED(wgrad_big_kernel, 2);
-        else if (bt)
-            GSK_GROUPED(rows_big_kernel, 2, LINES);
-        else
-            GSK_GROUPED(rows_big_kernel, 2, KROWS);
+        GSK_GROUPED_16(2);
     }
+#undef GSK_GROUPED_16
 #undef GSK_GROUPED
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) {

@@ -28,7 +28,7 @@ from dataclasses import dataclass
 import torch
 
 from ._lib import (BF16, F16, F32, FLAG_C_INPUT_DTYPE, GROUPED_ROWS, GROUPED_ROWS_BT,
-                   GROUPED_WGRAD, Grouped, last_error, load)
+                   GROUPED_WGRAD, Adapter, Grouped, last_error, load)
 
 _CODES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
@@ -268,3 +268,43 @@ def grouped_matmul_wgrad(a, dc, offsets, out_dtype=None):
     groups, K, N = offsets.numel() - 1, a.shape[1], dc.shape[1]
     c = torch.empty((groups, K, N), dtype=c_type, device=dev)
     return _grouped(dev, GROUPED_WGRAD, a, dc, c, offsets, K, N, groups, flags)
+
+
+def adapter_matmul(x, w, a, b, ids, scales=None, out_dtype=None):
+    """y[t] = x[t] @ w + scales[i] * (x[t] @ a[i].T) @ b[i].T with i = ids[t],
+    and x[t] @ w alone for an id outside [0, adapters): a shared projection
+    with each request's low-rank adapter, rows in any order.  ``w`` is K x N,
+    contiguous or the transposed view of a contiguous N x K linear-layer weight
+    (read as it lies); ``a`` adapters x rank x K and ``b`` adapters x N x rank
+    are the two small layers' weights; ``ids`` is int32, ``scales`` float32 per
+    adapter (None: all 1).  y is fp32, or x's dtype when ``out_dtype`` is x's
+    dtype.  A serving call, without a gradient."""
+    dev = _gpu("adapter_matmul", x, w, a, b, ids, *([] if scales is None else [scales]))
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[0]:
+        raise ValueError(f"incompatible shapes {tuple(x.shape)} and {tuple(w.shape)}")
+    (T, K), N = x.shape, w.shape[1]
+    if a.dim() != 3 or b.dim() != 3 or a.shape[2] != K or \
+            b.shape != (a.shape[0], N, a.shape[1]):
+        raise ValueError(f"a must be adapters x rank x {K} and b adapters x {N} x rank, got "
+                         f"{tuple(a.shape)} and {tuple(b.shape)}")
+    if not x.dtype == w.dtype == a.dtype == b.dtype:
+        raise ValueError(f"x, w, a and b differ in dtype: {x.dtype}, {w.dtype}, {a.dtype}, {b.dtype}")
+    _code(x, "x")
+    if ids.dtype != torch.int32 or ids.shape != (T,):
+        raise ValueError(f"ids must be int32 and ({T},), got {ids.dtype} {tuple(ids.shape)}")
+    if scales is not None and (scales.dtype != torch.float32 or scales.shape != (a.shape[0],)):
+        raise ValueError(f"scales must be float32 and ({a.shape[0]},), got {scales.dtype} "
+                         f"{tuple(scales.shape)}")
+    c_type, flags = _c_flags(x.dtype, out_dtype)
+    x = _dense(x)
+    trans = not w.is_contiguous() and w.t().is_contiguous()
+    w = _dense(w.t() if trans else w)
+    a, b, ids = a.contiguous(), b.contiguous(), ids.contiguous()
+    scales = None if scales is None else scales.contiguous()
+    y = torch.empty((T, N), dtype=c_type, device=dev)
+    lib = load()
+    p = Adapter(_CODES[x.dtype], a.shape[1], T, K, N, a.shape[0], trans, flags)
+    ws = _bytes(lib.gemm_adapter_workspace_size(ctypes.byref(p)), dev)
+    _call(dev, lib.gemm_adapter_run, ctypes.byref(p), x.data_ptr(), w.data_ptr(), a.data_ptr(),
+          b.data_ptr(), ids.data_ptr(), _ptr(scales), y.data_ptr(), _ptr(ws))
+    return y

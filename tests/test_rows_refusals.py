@@ -8,7 +8,7 @@ import torch
 
 import persistent_stream_tiling_amd as gsk
 from persistent_stream_tiling_amd import _lib
-from persistent_stream_tiling_amd._lib import Grouped, last_error
+from persistent_stream_tiling_amd._lib import Adapter, Grouped, last_error
 
 P = 0x1000  # an aligned address that nothing reads
 
@@ -113,19 +113,50 @@ def test_grouped_refuses(lib):
     assert run(op=2, K=0, A=None, C=None) == 0
 
 
+def test_adapter_refuses(lib):
+    def run(dtype=_lib.BF16, rank=8, rows=64, K=32, N=16, adapters=4, trans=0, flags=0, X=P, W=P,
+            A=P, B=P, ids=P, scales=None, Y=P, ws=P):
+        p = Adapter(dtype, rank, rows, K, N, adapters, trans, flags)
+        return lib.gemm_adapter_run(ctypes.byref(p), X, W, A, B, ids, scales, Y, ws, None)
+
+    refused(lib.gemm_adapter_run(None, P, P, P, P, P, None, P, P, None), "NULL problem")
+    refused(run(dtype=_lib.I8), "fp32, fp16 or bf16")
+    refused(run(flags=_lib.FLAG_ONE_TILE), "GEMM_FLAG_C_INPUT_DTYPE")
+    for kw in (dict(rows=-1), dict(K=-1), dict(N=-1), dict(adapters=-1)):
+        refused(run(**kw), "must not be negative")
+    for rank in (0, -3, 129):
+        refused(run(rank=rank), "rank must be between 1 and 128")
+    for kw in (dict(rows=2 ** 24), dict(K=2 ** 20), dict(N=2 ** 20)):
+        refused(run(**kw), "must stay below")
+    for name in ("X", "W", "A", "B", "ids", "Y"):
+        refused(run(**{name: None}), "NULL")
+        refused(run(**{name: P + 1}), "misaligned")
+    refused(run(scales=P + 2), "misaligned")
+    refused(run(X=P + 8), "misaligned")
+    refused(run(ws=P + 16), "misaligned")
+    refused(run(ws=None), "bytes of workspace", -2)
+    assert run(rows=0, X=None, ids=None, Y=None, ws=None) == 0
+    assert run(N=0, W=None, Y=None, ws=None) == 0
+    big = Adapter(_lib.BF16, 8, 64, 32, 16, 4, 0, 0)
+    assert lib.gemm_adapter_workspace_size(ctypes.byref(big)) > 0
+    assert lib.gemm_adapter_workspace_size(None) == 0
+
+
 def test_struct_layout_matches_the_header(tmp_path):
     import os
     import subprocess
     src = tmp_path / "sizes.c"
     src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "gemm_sk.h"\nint main(void)'
-                   '{printf("%zu %zu %zu", sizeof(gemm_grouped), offsetof(gemm_grouped, rows), '
-                   'offsetof(gemm_grouped, flags)); return 0;}')
+                   '{printf("%zu %zu %zu %zu %zu %zu", sizeof(gemm_grouped), offsetof(gemm_grouped, rows), '
+                   'offsetof(gemm_grouped, flags), sizeof(gemm_adapter), '
+                   'offsetof(gemm_adapter, rows), offsetof(gemm_adapter, flags)); return 0;}')
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o",
                     str(tmp_path / "sizes")], check=True)
     got = subprocess.run([str(tmp_path / "sizes")], capture_output=True, text=True).stdout.split()
     assert [int(v) for v in got] == [ctypes.sizeof(Grouped), Grouped.rows.offset,
-                                     Grouped.flags.offset]
+                                     Grouped.flags.offset, ctypes.sizeof(Adapter),
+                                     Adapter.rows.offset, Adapter.flags.offset]
 
 
 def test_python_calls_refuse_tensors_off_the_gpu():
