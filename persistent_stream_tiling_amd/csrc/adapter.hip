@@ -19,8 +19,6 @@ using namespace dev;
 
 namespace {
 
-typedef float f32x2v __attribute__((ext_vector_type(2)));
-
 struct AdapterArgs {
     const uint8_t *X;        // rows x ldx
     const uint8_t *W;        // K x ldw, or N x ldw (linear-layer weights)
@@ -36,7 +34,8 @@ struct AdapterArgs {
     int32_t rows, N, K, rank, rank_pad, adapters;
     int32_t ldx, ldw;
     int32_t slices, slice_k; // of the rank projection's depth
-    int32_t parts, part_k;   // of the shared product's depth
+    int32_t parts, part_k;   // workgroups per tile; depth of each of the first k_parts
+    int32_t k_parts;         // the others add adapters only (parts = 1: one does both)
     int32_t terms;           // 16-bit terms that H is split into
     int32_t tiles_m, tiles_n;
     int32_t c_dtype, c_vec, xcds;
@@ -48,6 +47,39 @@ __device__ __forceinline__ int adapter_of(const AdapterArgs &a, int row)
     const int id = row < a.rows ? a.ids[row] : -1;
     return id >= 0 && id < a.adapters ? id : -1;
 }
+
+// The distinct adapters among up to 64 rows, lane l holding row l's (-1: none).
+// Rows of one adapter find each other bit by bit, all at once; the lowest of
+// them stands for it, and adapters are numbered in the order of those rows.
+struct Present {
+    int id;
+    uint64_t same;   // rows of the lane's adapter
+    int rank;        // its number, if the lane's row is the lowest; else -1
+    int count;
+
+    __device__ __forceinline__ Present(int id_, int adapters) : id(id_)
+    {
+        const int lane = threadIdx.x & 63;
+        same = __builtin_amdgcn_ballot_w64(id >= 0);
+        for (int b = 0; (adapters - 1) >> b > 0; ++b) {
+            const bool one = (id >> b) & 1;
+            const uint64_t m = __builtin_amdgcn_ballot_w64(one);
+            same &= one ? m : ~m;
+        }
+        const bool lowest = id >= 0 && (same & ((1ull << lane) - 1)) == 0;
+        const uint64_t all = __builtin_amdgcn_ballot_w64(lowest);
+        rank = lowest ? __builtin_popcountll(all & ((1ull << lane) - 1)) : -1;
+        count = __builtin_popcountll(all);
+    }
+    // adapter number n (below count) and its rows
+    __device__ __forceinline__ int nth(int n, uint64_t *rows) const
+    {
+        const int r = __builtin_ctzll(__builtin_amdgcn_ballot_w64(rank == n));
+        *rows = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)same, r) |
+                (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(same >> 32), r) << 32;
+        return __builtin_amdgcn_readlane(id, r);
+    }
+};
 
 template <int DT>
 struct Elem;
@@ -89,253 +121,375 @@ __device__ __forceinline__ u32x4 load_some(const T *p, int n)
 }
 
 // ---------------------------------------------------------------------------
-// H[t] = s[a] X[t] . A[a]^T, 16 rows and one slice of the depth per workgroup
-// of eight waves.
+// H[t] = s[a] X[t] . A[a]^T: 16 RB rows and one slice of the depth per
+// workgroup.
 //
-// The waves share the adapters present among the 16 rows out between them, and
-// where there are fewer than eight, the depth as well; a wave multiplies all 16
-// rows by one adapter's A (16x16 matrix instruction: 16 ranks by 16 rows) and
-// keeps the rows that chose it.  So a row's sums hold nothing of another
-// adapter's values, and neither does a row without one.  Operands go straight
-// from memory to registers, 16 bytes per lane and load: each is used once.
-// Bound by the reads of X and of the A present; a decoding step (32 rows of K =
-// 4096, each with its own adapter) spreads them over 2 x 16 workgroups by
-// slices, whose sums the second launch adds in order.
-constexpr int kShrinkRows = 16, kShrinkWaves = 8;
+// The waves share the adapters present among the rows out between them and,
+// where there are fewer adapters than waves, the depth as well; a wave
+// multiplies all the rows by one adapter's A (16x16 matrix instruction: 16
+// ranks by 16 rows) and keeps the rows that chose it.  So a row's sums hold
+// nothing of another adapter's values.  Operands go straight from memory to
+// registers, 16 bytes per lane and load, rounds of them in flight together:
+// what bounds this is the latency of a few dependent round trips (ids, then
+// operands), and with many rows the reads of A, which RB = 2 halves.  Slices
+// (blockIdx.y) fill the chip; their sums are added, in order, by the second
+// launch.
+constexpr int shrink_waves(int rt, int rb) { return rt * rb <= 4 ? 16 : 64 / (rt * rb); }
 
-template <int DT, int RT>  // RT: 16-rank blocks
-__global__ __launch_bounds__(64 * kShrinkWaves) void shrink_kernel(AdapterArgs a)
+template <int DT, int RT, int RB>  // RT: 16-rank blocks, RB: 16-row blocks
+__global__ __launch_bounds__(64 * shrink_waves(RT, RB)) void shrink_kernel(AdapterArgs a)
 {
     using T = typename Elem<DT>::T;
     constexpr int V = 16 / (int)sizeof(T);  // elements per load; a step is 4 V deep
+    constexpr int NW = shrink_waves(RT, RB), kRows = 16 * RB;
     constexpr int kPitch = RT * 16 + 4;
-    __shared__ __attribute__((aligned(16))) float red[kShrinkWaves][kShrinkRows][kPitch];
+    constexpr int kAhead = RT == 1 ? 8 : (RT == 8 ? 2 : 4);  // steps per round
+    __shared__ __attribute__((aligned(16))) float red[NW][kRows][kPitch];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int r16 = lane & 15, q = lane >> 4;
-    const int row0 = (int)blockIdx.x * kShrinkRows;
+    const int row0 = (int)blockIdx.x * kRows;
     if (a.parts > 1)
-        for (int i = (int)(blockIdx.y * gridDim.x + blockIdx.x) * 64 * kShrinkWaves +
-                     (int)threadIdx.x;
-             i < a.tiles_m * a.tiles_n; i += (int)(gridDim.x * gridDim.y) * 64 * kShrinkWaves)
+        for (int i = (int)(blockIdx.y * gridDim.x + blockIdx.x) * 64 * NW + (int)threadIdx.x;
+             i < a.tiles_m * a.tiles_n; i += (int)(gridDim.x * gridDim.y) * 64 * NW)
             a.counters[i] = 0;
 
-    const int id = adapter_of(a, row0 + r16);
-    uint64_t left = __builtin_amdgcn_ballot_w64(id >= 0) & 0xffff;
-    int n = 0;
-    for (uint64_t m = left; m; ++n)
-        m &= ~__builtin_amdgcn_ballot_w64(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(m)));
-    if (n == 0)
+    int id[RB];
+    uint32_t has = 0;  // bit r: row row0 + r has an adapter
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        id[b] = adapter_of(a, row0 + 16 * b + r16);
+        has |= (uint32_t)(__builtin_amdgcn_ballot_w64(id[b] >= 0) & 0xffff) << (16 * b);
+    }
+    if (has == 0)
         return;  // nobody reads these rows' H
-    const int ways = n < kShrinkWaves ? kShrinkWaves / n : 1;  // of the depth, per adapter
+    float scale[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+        scale[b] = a.scales && id[b] >= 0 ? a.scales[id[b]] : 1.0f;
+    const Present present(lane < kRows ? adapter_of(a, row0 + lane) : -1, a.adapters);
+    const int n = present.count;
+    const int ways = n < NW ? NW / n : 1;  // of the depth, per adapter
     const int k_lo = (int)blockIdx.y * a.slice_k;
     const int k_hi = k_lo + a.slice_k < a.K ? k_lo + a.slice_k : a.K;
-    const int way = wave / n;  // (n < 8: waves past n * ways idle)
+    const int way = n < NW ? wave / n : 0;  // (waves past n * ways idle)
     const int per = ((k_hi - k_lo + ways - 1) / ways + 4 * V - 1) / (4 * V) * (4 * V);
     const int k0 = k_lo + way * per;
     const int k1 = k0 + per < k_hi ? k0 + per : k_hi;
 
-    const T *x = (const T *)a.x_plain + (int64_t)(row0 + r16) * a.K;
-    const bool x_ok = row0 + r16 < a.rows;
-    int nth = 0;
-    for (uint64_t m = left; m; ++nth) {
-        const int mine = __builtin_amdgcn_readlane(id, __builtin_ctzll(m));
-        m &= ~__builtin_amdgcn_ballot_w64(id == mine);
-        if (n < kShrinkWaves ? (way >= ways || wave - way * n != nth) : nth % kShrinkWaves != wave)
-            continue;
-        f32x4 acc[RT];
+    // Rows and ranks that do not exist repeat the last one that does: their
+    // sums go nowhere.
+    const T *xp[RB];
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
-            acc[t] = f32x4{};
-        const T *A = (const T *)a.A + (int64_t)mine * a.rank * a.K;
-#pragma unroll 2
-        for (int k = k0; k < k1; k += 4 * V) {
-            const int kk = k + q * V;
-            const u32x4 fx = load_some(x + kk, x_ok ? k1 - kk : 0);
-            u32x4 fa[RT];
+    for (int b = 0; b < RB; ++b) {
+        const int row = row0 + 16 * b + r16;
+        xp[b] = (const T *)a.x_plain + (int64_t)(row < a.rows ? row : a.rows - 1) * a.K + q * V;
+    }
+    for (int nth = n < NW ? wave - way * n : wave; way < ways && nth < n; nth += NW) {
+        uint64_t rows;
+        const int mine = present.nth(nth, &rows);
+        f32x4 acc[RB][RT];
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                const int r = t * 16 + r16;
-                fa[t] = load_some(A + (int64_t)r * a.K + kk, r < a.rank ? k1 - kk : 0);
-            }
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                if constexpr (DT == 1) {
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                        __builtin_bit_cast(f16x8, fa[t]), __builtin_bit_cast(f16x8, fx), acc[t], 0, 0, 0);
-                } else if constexpr (DT == 2) {
-                    acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, fa[t]), __builtin_bit_cast(bf16x8, fx), acc[t], 0, 0, 0);
-                } else {
-                    // element e of both operands: the same k meets the same k
-                    const f32x4 af = __builtin_bit_cast(f32x4, fa[t]), xf = __builtin_bit_cast(f32x4, fx);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(af[e], xf[e], acc[t], 0, 0, 0);
-                }
-            }
-        }
-        // lane: row r16, ranks 16 t + 4 q .. + 3
-        if (id == mine)
+        for (int b = 0; b < RB; ++b)
 #pragma unroll
             for (int t = 0; t < RT; ++t)
-                *(f32x4 *)&red[n < kShrinkWaves ? way : 0][r16][t * 16 + 4 * q] = acc[t];
+                acc[b][t] = f32x4{};
+        const T *ap[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const int r = t * 16 + r16;
+            ap[t] = (const T *)a.A + ((int64_t)mine * a.rank + (r < a.rank ? r : a.rank - 1)) * a.K + q * V;
+        }
+        const auto step = [&](const u32x4 (&fx)[RB], const u32x4 (&fa)[RT]) {
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    if constexpr (DT == 1) {
+                        acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            __builtin_bit_cast(f16x8, fa[t]), __builtin_bit_cast(f16x8, fx[b]),
+                            acc[b][t], 0, 0, 0);
+                    } else if constexpr (DT == 2) {
+                        acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, fa[t]), __builtin_bit_cast(bf16x8, fx[b]),
+                            acc[b][t], 0, 0, 0);
+                    } else {
+                        // element e of both operands: the same k meets the same k
+                        const f32x4 af = __builtin_bit_cast(f32x4, fa[t]);
+                        const f32x4 xf = __builtin_bit_cast(f32x4, fx[b]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(af[e], xf[e], acc[b][t],
+                                                                             0, 0, 0);
+                    }
+                }
+        };
+        int k = k0;
+        for (; k + kAhead * 4 * V <= k1; k += kAhead * 4 * V) {
+            u32x4 fx[kAhead][RB], fa[kAhead][RT];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+                    fx[i][b] = load_some(xp[b] + k + i * 4 * V, V);
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    fa[i][t] = load_some(ap[t] + k + i * 4 * V, V);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                step(fx[i], fa[i]);
+        }
+        for (; k < k1; k += 4 * V) {
+            const int n_k = k1 - k - q * V;
+            u32x4 fx[RB], fa[RT];
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+                fx[b] = load_some(xp[b] + k, n_k);
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                fa[t] = load_some(ap[t] + k, n_k);
+            step(fx, fa);
+        }
+        // lane: row r16 of a block, ranks 16 t + 4 q .. + 3
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+            if (id[b] == mine)
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    *(f32x4 *)&red[way][16 * b + r16][t * 16 + 4 * q] = acc[b][t] * scale[b];
     }
     __syncthreads();
-    float *h = a.H + (int64_t)blockIdx.y * a.rows * a.rank_pad;
-    for (int i = threadIdx.x; i < kShrinkRows * RT * 16; i += 64 * kShrinkWaves) {
+    float *h = a.H + ((int64_t)blockIdx.y * a.rows + row0) * a.rank_pad;
+    for (int i = threadIdx.x; i < kRows * RT * 16; i += 64 * NW) {
         const int row = i / (RT * 16), r = i % (RT * 16);
-        const int of = adapter_of(a, row0 + row);
-        if (of < 0 || r >= a.rank_pad)
+        if (!((has >> row) & 1) || r >= a.rank_pad)
             continue;
         float sum = red[0][row][r];
         for (int w = 1; w < ways; ++w)
             sum += red[w][row][r];
-        h[(int64_t)(row0 + row) * a.rank_pad + r] = sum * (a.scales ? a.scales[of] : 1.0f);
+        // (the ranks past the last one are zero, whatever was multiplied there)
+        h[(int64_t)row * a.rank_pad + r] = r < a.rank ? sum : 0.0f;
     }
 }
 
 // ---------------------------------------------------------------------------
-// acc += H . B^T for the rows that have an adapter: row blocks of 32 from row0
-// on, column blocks of 32 from col0 on.  Of the adapters met in a wave's rows,
-// this call takes those numbered `part`, part + parts, ...
+// acc += H . B^T for the rows that have an adapter, by all waves of a workgroup
+// together: the tile's ROWS rows from m0 on; the wave's blocks of 32 x 32 start
+// at row `row0` of the tile and column col0 of C.  Of the adapters met in a
+// wave's rows, this call takes those numbered `part`, part + parts, ...
 //
-// Per adapter and 16 ranks, one matrix product of all the block's rows is
-// formed in registers of its own, and the rows that chose the adapter add it
-// to theirs: another adapter's infinities and NaN never reach them.  H is fp32
-// and the instruction takes 16 bits, so H is scaled by a power of two per row
-// (largest magnitude of the 16 near 2^10: inside fp16's range, the terms above
-// its subnormals) and split into 16-bit terms, each the rounding of what the
-// earlier ones leave: two for fp16 (22 bits) and for bf16 with bf16 results
-// (16 bits, against the 8 of the result), three for bf16 with fp32 results (24).
-// The fp32 kernel multiplies H as it is.
-template <int DT, int MT, int NT>
-__device__ __forceinline__ void add_adapters(f32x16 (&acc)[MT][NT], const AdapterArgs &a, int row0,
-                                             int col0, int part, int parts)
+// H is fp32 and the instruction takes 16 bits, so H is split into 16-bit terms,
+// each the rounding of what the earlier ones leave: two for fp16 (22 bits) and
+// for bf16 with bf16 results (16 bits, against the 8 of the result), three for
+// bf16 with fp32 results (24).  fp16 has not fp32's range: 16 ranks of a row
+// whose largest magnitude lies outside [2^-4, 2^15) are scaled by a power of
+// two to bring it near 2^10, and their products scaled back.  The workgroup
+// splits kChunk ranks of all its rows at a time, once, into LDS (the rings'
+// place).
+//
+// Where all rows of a 32-row block chose one adapter (prompts: long runs of
+// rows) and none is scaled, the products are added to the sums directly.
+// Otherwise a product of all the block's rows is formed in registers of its
+// own, and the rows that chose the adapter add it to theirs: so another
+// adapter's infinities and NaN never reach them.  The fp32 kernel multiplies H
+// as it is.
+// (ranks at a time: what the registers beside the sums hold)
+constexpr int rank_chunk(int nt) { return nt == 1 ? 64 : 32; }
+
+constexpr int kTermsOf(int dt) { return dt == 2 ? 3 : 2; }  // 16-byte words of 8 ranks (fp32: as they are)
+
+// LDS for ROWS rows: terms, then the scale of each row's 16 ranks.
+template <int DT, int ROWS, int NT>
+constexpr int adapters_lds()
+{
+    return ROWS * (kTermsOf(DT) * rank_chunk(NT) * 2 + rank_chunk(NT) / 16 * 4);
+}
+
+// Splits ranks r0 .. r0 + 16 groups - 1 of the tile's ROWS rows from m0 on into
+// terms in LDS, by all threads of the workgroup:
+//   terms [term][16 ranks][8 of them][row], 16 bytes each (fp32: the two
+//   "terms" are ranks 0-3 and 4-7 of the 8),
+//   scales [16 ranks][row] (fp16).
+// Rows without an adapter are zero.
+template <int ROWS>
+__device__ __forceinline__ int term_at(int chunk, int s, int g, int h, int row)
+{
+    return ((s * (chunk / 16) + g) * 2 + h) * ROWS + row;
+}
+
+template <int DT, int ROWS, int CHUNK>
+__device__ __forceinline__ void split_h(const AdapterArgs &a, uint8_t *lds, int m0, int r0, int groups)
 {
     using T = typename Elem<DT>::T;
-    constexpr int kTerms = DT == 2 ? 3 : 2;
-    const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
-    int id[MT];
-    uint64_t any = 0;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        id[i] = adapter_of(a, row0 + 32 * i + l32);
-        any |= __builtin_amdgcn_ballot_w64(id[i] >= 0);
-    }
-    if (!any)
-        return;
-    for (int r0 = 0; r0 < a.rank; r0 += 16) {
-        // the lane's H values: row l32 of each block, ranks r0 + 8 half .. + 7
-        float h[MT][8], up[MT];
-        u32x4 fh[MT][kTerms];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                h[i][e] = 0.0f;
-            if (id[i] >= 0) {
-                const float *p = a.H + (int64_t)(row0 + 32 * i + l32) * a.rank_pad + r0 + 8 * half;
-                for (int s = 0; s < a.slices; ++s, p += (int64_t)a.rows * a.rank_pad) {
-                    const f32x4 lo = *(const f32x4 *)p, hi = *(const f32x4 *)(p + 4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        h[i][e] += lo[e];
-                        h[i][4 + e] += hi[e];
+    constexpr int kTerms = kTermsOf(DT);
+    u32x4 *const terms = (u32x4 *)lds;
+    float *const scales = (float *)(lds + ROWS * kTerms * CHUNK * 2);
+    const auto at = [](int s, int g, int h, int row) { return term_at<ROWS>(CHUNK, s, g, h, row); };
+            // four ranks per thread: neighbouring lanes hold one row's 16
+            for (int item = threadIdx.x; item < ROWS * groups * 4; item += (int)blockDim.x) {
+                const int quad = item & 3, row = (item >> 2) % ROWS, g = (item >> 2) / ROWS;
+                f32x4 h = f32x4{};
+                if (adapter_of(a, m0 + row) >= 0) {
+                    // the slices in order, eight in flight together
+                    const float *p = a.H + (int64_t)(m0 + row) * a.rank_pad + r0 + 16 * g + 4 * quad;
+                    const int64_t next = (int64_t)a.rows * a.rank_pad;
+                    for (int s0 = 0; s0 < a.slices; s0 += 8) {
+                        f32x4 v[8];
+    #pragma unroll
+                        for (int s = 0; s < 8; ++s)
+                            v[s] = *(const f32x4 *)(p + (s0 + s < a.slices ? s0 + s : s0) * next);
+    #pragma unroll
+                        for (int s = 0; s < 8; ++s)
+    #pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                h[e] += s0 + s < a.slices ? v[s][e] : 0.0f;
                     }
                 }
-            }
-        }
-        if constexpr (DT != 0) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                float top = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    top = fmaxf(top, fabsf(h[i][e]));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                int ex = (int)((bits_of(top) >> 23) & 255) - 137;  // top = 2^(ex + 10) * [1, 2)
-                ex = top < __builtin_inff() ? (ex < -100 ? -100 : ex) : 0;
-                const float down = __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23);
-                up[i] = __builtin_bit_cast(float, (uint32_t)(127 + ex) << 23);
-                T t[kTerms][8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float rest = h[i][e] * down;
-#pragma unroll
+                if constexpr (DT == 0) {
+                    terms[at(quad & 1, g, quad >> 1, row)] = __builtin_bit_cast(u32x4, h);
+                } else {
+                    float down = 1.0f;
+                    if constexpr (DT == 1) {
+                        float top = fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3])));
+                        top = fmaxf(top, __shfl_xor(top, 1));
+                        top = fmaxf(top, __shfl_xor(top, 2));
+                        float up = 1.0f;
+                        if (top > 0.0f && (top < 0.0625f || top >= 32768.0f) && top < __builtin_inff()) {
+                            int ex = (int)((bits_of(top) >> 23) & 255) - 137;  // top: 2^(ex + 10) * [1, 2)
+                            ex = ex < -100 ? -100 : ex;
+                            down = __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23);
+                            up = __builtin_bit_cast(float, (uint32_t)(127 + ex) << 23);
+                        }
+                        scales[g * ROWS + row] = up;  // (all four lanes the same)
+                    }
+                    float x[4];
+    #pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = h[e] * down;
+    #pragma unroll
                     for (int s = 0; s < kTerms; ++s) {
-                        t[s][e] = (T)rest;
-                        // (an infinity or NaN leaves nothing for the later terms)
-                        rest = fabsf(rest) < __builtin_inff() ? rest - (float)t[s][e] : 0.0f;
+                        T t[4];
+    #pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            t[e] = (T)x[e];
+                            // (an infinity or NaN leaves nothing for the later terms)
+                            x[e] = fabsf(x[e]) < __builtin_inff() ? x[e] - (float)t[e] : 0.0f;
+                        }
+                        u32x2 w;
+                        __builtin_memcpy(&w, t, 8);
+                        ((u32x2 *)&terms[at(s, g, quad >> 1, row)])[quad & 1] = w;
                     }
                 }
-#pragma unroll
-                for (int s = 0; s < kTerms; ++s)
-                    __builtin_memcpy(&fh[i][s], t[s], 16);
             }
-        }
-        uint64_t left[MT];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-            left[i] = __builtin_amdgcn_ballot_w64(id[i] >= 0) & 0xffffffffull;
-        for (int nth = 0;; ++nth) {
-            // the first row still waiting names the adapter
-            int mine = -1;
-#pragma unroll
-            for (int i = MT - 1; i >= 0; --i)
-                if (left[i])
-                    mine = __builtin_amdgcn_readlane(id[i], __builtin_ctzll(left[i]));
-            if (mine < 0)
-                break;
-            uint64_t here[MT];
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                here[i] = __builtin_amdgcn_ballot_w64(id[i] == mine) & 0xffffffffull;
-                left[i] &= ~here[i];
-            }
-            if (nth % parts != part)
-                continue;
+}
+
+template <int DT, int ROWS, int MT, int NT>
+__device__ __forceinline__ void add_adapters(f32x16 (&acc)[MT ? MT : 1][NT], const AdapterArgs &a,
+                                             uint8_t *lds, int m0, int row0, int col0, int part,
+                                             int parts)
+{
+    using T = typename Elem<DT>::T;
+    constexpr int kTerms = kTermsOf(DT), kChunk = rank_chunk(NT), kGroups = kChunk / 16;
+    constexpr int kB = DT == 0 ? 2 : 1;  // 16-byte words of 8 ranks
+    constexpr int kTogether = NT == 1 && MT < 4 ? 4 : 2;  // adapters whose B is loaded at once
+    const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+    const u32x4 *const terms = (const u32x4 *)lds;
+    const float *const scales = (const float *)(lds + ROWS * kTerms * kChunk * 2);
+    const auto at = [](int s, int g, int h, int row) { return term_at<ROWS>(kChunk, s, g, h, row); };
+
+    for (int r0 = 0; r0 < a.rank; r0 += kChunk) {
+        const int groups = a.rank - r0 < kChunk ? (a.rank - r0 + 15) / 16 : kGroups;
+        __syncthreads();  // nobody reads the LDS any more
+        split_h<DT, ROWS, kChunk>(a, lds, m0, r0, groups);
+        __syncthreads();
+
+        // the wave's columns of one adapter's B: lane n, 8 ranks per half
+        const auto load_b = [&](u32x4 (&fb)[kGroups][NT][kB], int mine) {
             const T *B = (const T *)a.B + (int64_t)mine * a.N * a.rank;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int n = col0 + 32 * j + l32;
-                if constexpr (DT != 0) {
-                    const int k = r0 + 8 * half;
-                    const u32x4 fb = load_some(B + (int64_t)n * a.rank + k, n < a.N ? a.rank - k : 0);
+            for (int g = 0; g < kGroups; ++g)
+                if (g < groups)
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        if (!here[i])
+                    for (int j = 0; j < NT; ++j) {
+                        const int n = col0 + 32 * j + l32, k = r0 + 16 * g + 8 * half;
+                        const int have = n < a.N ? a.rank - k : 0;
+#pragma unroll
+                        for (int q = 0; q < kB; ++q)
+                            fb[g][j][q] = load_some(B + (int64_t)n * a.rank + k + 4 * q, have - 4 * q);
+                    }
+        };
+        // two row blocks at a time: their 64 rows are the lanes'
+#pragma unroll
+        for (int i0 = 0; i0 < MT; i0 += 2) {
+            constexpr int kRows = MT == 1 ? 32 : 64;
+            const int first = row0 + 32 * i0;
+            const Present present(lane < kRows ? adapter_of(a, m0 + first + lane) : -1, a.adapters);
+            const uint64_t exist = __builtin_amdgcn_ballot_w64(lane < kRows && m0 + first + lane < a.rows);
+            for (int nth = part; nth < present.count; nth += kTogether * parts) {
+                uint64_t rows_of[kTogether];
+                u32x4 fb_of[kTogether][kGroups][NT][kB];
+#pragma unroll
+                for (int t = 0; t < kTogether; ++t) {
+                    rows_of[t] = 0;
+                    if (nth + t * parts < present.count)
+                        load_b(fb_of[t], present.nth(nth + t * parts, &rows_of[t]));
+                }
+#pragma unroll
+                for (int t = 0; t < kTogether; ++t) {
+                    const uint64_t rows = rows_of[t];
+                    const u32x4 (&fb)[kGroups][NT][kB] = fb_of[t];
+#pragma unroll
+                    for (int i = 0; i < (MT == 1 ? 1 : 2); ++i) {
+                        const uint32_t here = (uint32_t)(rows >> (32 * i));
+                        if (!here)
                             continue;
-                        f32x16 sum = f32x16{};
-                        if constexpr (kTerms > 2)
-                            if (a.terms > 2)
-                                mfma16<DT>(sum, fb, fh[i][2]);
-                        mfma16<DT>(sum, fb, fh[i][1]);
-                        mfma16<DT>(sum, fb, fh[i][0]);
+                        const bool chose = (here >> l32) & 1, all = here == (uint32_t)(exist >> (32 * i));
+                        const int row = first + 32 * i + l32;
 #pragma unroll
-                        for (int v = 0; v < 16; ++v)
-                            acc[i][j][v] = id[i] == mine ? __builtin_fmaf(sum[v], up[i], acc[i][j][v])
-                                                         : acc[i][j][v];
+                        for (int g = 0; g < kGroups; ++g) {
+                            if (g >= groups)
+                                continue;
+                            u32x4 fh[kTerms];
+#pragma unroll
+                            for (int s = 0; s < kTerms; ++s)
+                                fh[s] = terms[at(s, g, half, row)];
+                            const float up = DT == 1 ? scales[g * ROWS + row] : 1.0f;
+                            const auto multiply = [&](f32x16 &sum, int j) {
+                                if constexpr (DT == 0) {
+                                    // ranks 8 half + e of both operands meet in instruction e
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) {
+                                        const f32x4 x = __builtin_bit_cast(f32x4, fb[g][j][e >> 2]);
+                                        const f32x4 y = __builtin_bit_cast(f32x4, fh[e >> 2]);
+                                        sum = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e & 3], y[e & 3], sum,
+                                                                                   0, 0, 0);
+                                    }
+                                } else {
+                                    if constexpr (kTerms > 2)
+                                        if (a.terms > 2)
+                                            mfma16<DT>(sum, fb[g][j][0], fh[2]);
+                                    mfma16<DT>(sum, fb[g][j][0], fh[1]);
+                                    mfma16<DT>(sum, fb[g][j][0], fh[0]);
+                                }
+                            };
+                            if (all && (DT != 1 || __builtin_amdgcn_ballot_w64(up != 1.0f) == 0)) {
+#pragma unroll
+                                for (int j = 0; j < NT; ++j)
+                                    multiply(acc[i0 + i][j], j);
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < NT; ++j) {
+                                    f32x16 sum = f32x16{};
+                                    multiply(sum, j);
+                                    f32x16 &to = acc[i0 + i][j];
+#pragma unroll
+                                    for (int v = 0; v < 16; ++v)
+                                        to[v] = chose ? __builtin_fmaf(sum[v], up, to[v]) : to[v];
+                                }
+                            }
+                        }
                     }
-                } else {
-                    // ranks r0 + 8 half + e of both operands meet in instruction e
-                    f32x16 sum[MT];
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-                        sum[i] = f32x16{};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int k = r0 + 8 * half + e;
-                        const float fb = n < a.N && k < a.rank ? (float)B[(int64_t)n * a.rank + k] : 0.0f;
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-                            sum[i] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb, h[i][e], sum[i], 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int v = 0; v < 16; ++v)
-                            acc[i][j][v] = id[i] == mine ? acc[i][j][v] + sum[i][v] : acc[i][j][v];
                 }
             }
         }
@@ -383,7 +537,8 @@ __device__ __forceinline__ TileWork shared_work(const AdapterArgs &a, int m0, in
 template <int DT, int LB>
 __global__ __launch_bounds__(512, 1) void adapter_big_kernel(AdapterArgs a)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[(ring_of(LINES) + ring_of(LB)) * kPiece];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[(ring_of(0, LINES) + ring_of(1, LB)) * kPiece];
+    static_assert(adapters_lds<DT, kBig, 2>() <= sizeof(lds), "LDS");
     int tm, tn;
     if (!find_tile(a, (int)blockIdx.x, &tm, &tn))
         return;
@@ -391,84 +546,108 @@ __global__ __launch_bounds__(512, 1) void adapter_big_kernel(AdapterArgs a)
     const TileWork w = shared_work<LB>(a, m0, n0, 0, a.K);
     const __amdgpu_buffer_rsrc_t c = c_rows(a, m0);
     const bool vec = a.c_vec || n0 + kBig <= a.N;
-    big_tile<DT, LINES, LB>(w, lds, [&](f32x16 (&acc)[4][2], int row, int col) {
-        // (a row block at a time: all four at once do not fit the registers)
+    big_tile<DT, LINES, LB>(w, lds, [&](f32x16 (&acc)[4][2], auto blocks, int row, int col) {
+        constexpr int kBlocks = decltype(blocks)::value;
+        // (a group without rows takes part in the splitting of H)
+        add_adapters<DT, kBig, kBlocks, 2>(
+            reinterpret_cast<f32x16(&)[kBlocks ? kBlocks : 1][2]>(acc), a, lds, m0, row, n0 + col, 0, 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f32x16 blk[1][2] = {{acc[i][0], acc[i][1]}};
-            add_adapters<DT, 1, 2>(blk, a, m0 + row + 32 * i, n0 + col, 0, 1);
-            acc[i][0] = blk[0][0];
-            acc[i][1] = blk[0][1];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 2 * kBlocks; ++i)
             store_block(acc[i >> 1][i & 1], c, c_row_bytes(a), row + (i >> 1) * 32, w.m,
                         n0 + col + (i & 1) * 32, a.N, vec, a.c_dtype);
     });
 }
 
-// Few rows: 32 MT x 128 tiles, the depth cut into parts (blockIdx.y) where
-// there are too few tiles to fill the chip.  Each part parks its fp32 sums and
-// counts itself in; the last one adds all parts in their order, whichever it
-// is, so the result does not depend on who that was.
+// Parks one part's fp32 sums of a tile and counts it in.  True for the last
+// part to come, whose accumulators then hold the sum of all parts in their
+// order, whoever it is: the result does not depend on who that was.
+template <int MT, int NT>
+__device__ __forceinline__ bool join_parts(f32x16 (&acc)[MT][NT], const AdapterArgs &a, uint8_t *lds,
+                                           int part, int tile)
+{
+    // Slot layout: wave, block, quad, lane: 16-byte vectors side by side.  The
+    // stores and loads are coherent across the dies (sc1) and the waits below
+    // order them, so the counter can be relaxed: an agent-scope release or
+    // acquire would write back or drop the die's whole L2, and with it
+    // everybody's operand lines.
+    constexpr int kCoherent = 16, kQuads = MT * NT * 4;
+    constexpr int kTogether = kQuads <= 4 ? 8 : (kQuads <= 8 ? 4 : 2);  // parts read in one round
+    const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+    constexpr int kSlot = 256 * kQuads * 4;  // floats (256 threads)
+    const int tiles = a.tiles_m * a.tiles_n, off = (wave * kQuads * 64 + lane) * 16;
+    const auto slot = [&](int p) {
+        return make_rsrc(a.partials + ((int64_t)p * tiles + tile) * kSlot);
+    };
+    const __amdgpu_buffer_rsrc_t mine = slot(part);
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+        const f32x16 &x = acc[i / 4 / NT][i / 4 % NT];
+        const int g = 4 * (i & 3);
+        const u32x4 u = u32x4{bits_of(x[g]), bits_of(x[g + 1]), bits_of(x[g + 2]), bits_of(x[g + 3])};
+        __builtin_amdgcn_raw_buffer_store_b128(u, mine, off + i * 1024, 0, kCoherent);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    int32_t *arrived = (int32_t *)lds;  // (nobody reads the ring any more)
+    if (threadIdx.x == 0)
+        *arrived = __hip_atomic_fetch_add(a.counters + tile, 1, __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (*arrived != a.parts - 1)
+        return false;
+#pragma unroll
+    for (int i = 0; i < MT * NT; ++i)
+        acc[i / NT][i % NT] = f32x16{};
+    for (int p0 = 0; p0 < a.parts; p0 += kTogether) {
+        u32x4 v[kTogether][kQuads];
+#pragma unroll
+        for (int p = 0; p < kTogether; ++p) {
+            const __amdgpu_buffer_rsrc_t from = slot(p0 + p < a.parts ? p0 + p : p0);
+#pragma unroll
+            for (int i = 0; i < kQuads; ++i)
+                v[p][i] = __builtin_amdgcn_raw_buffer_load_b128(from, off + i * 1024, 0, kCoherent);
+        }
+#pragma unroll
+        for (int p = 0; p < kTogether; ++p)
+#pragma unroll
+            for (int i = 0; i < kQuads; ++i) {
+                const f32x4 f = __builtin_bit_cast(f32x4, v[p][i]);
+                f32x16 &x = acc[i / 4 / NT][i / 4 % NT];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[4 * (i & 3) + e] += p0 + p < a.parts ? f[e] : 0.0f;
+            }
+    }
+    return true;
+}
+
+// Few rows: 32 MT x 128 tiles, and several workgroups per tile (blockIdx.y)
+// where there are too few tiles to fill the chip: k_parts that share the depth,
+// and beside them some that add the adapters, so that neither waits for the
+// other.
 template <int DT, int LB, int MT>
 __global__ __launch_bounds__(256, 2) void adapter_narrow_kernel(AdapterArgs a)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[narrow_lds(MT)];
+    static_assert(adapters_lds<DT, 32 * MT, 1>() <= sizeof(lds), "LDS");
     int tm, tn;
     if (!find_tile(a, (int)blockIdx.x, &tm, &tn))
         return;
     const int m0 = tm * 32 * MT, n0 = tn * kNarrow, part = (int)blockIdx.y;
-    const int k0 = part * a.part_k;
+    const bool shared = part < a.k_parts;
+    const int k0 = shared ? part * a.part_k : 0;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    const TileWork w =
-        shared_work<LB>(a, m0, n0, k0, a.K - k0 < a.part_k ? a.K - k0 : a.part_k);
+    const int k = a.K - k0 < a.part_k ? a.K - k0 : a.part_k;
+    const TileWork w = shared_work<LB>(a, m0, n0, k0, shared ? k : 0);
     f32x16 acc[MT][1];
     narrow_tile<DT, LB, MT>(acc, w, lds);
-    add_adapters<DT, MT, 1>(acc, a, m0, n0 + wave * 32, part, a.parts);
-    if (a.parts > 1) {
-        // slot layout: wave, block, quad, lane: 16-byte vectors side by side.
-        // The stores and loads are coherent across the dies (sc1).
-        constexpr int kCoherent = 16, kSlot = MT * 32 * kNarrow;
-        const int tiles = a.tiles_m * a.tiles_n, tile = tm * a.tiles_n + tn;
-        const __amdgpu_buffer_rsrc_t slot = make_rsrc(a.partials + ((int64_t)part * tiles + tile) * kSlot);
-        const int off = (wave * MT * 4 * 64 + lane) * 16;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const u32x4 u = u32x4{bits_of(acc[i][0][4 * g]), bits_of(acc[i][0][4 * g + 1]),
-                                      bits_of(acc[i][0][4 * g + 2]), bits_of(acc[i][0][4 * g + 3])};
-                __builtin_amdgcn_raw_buffer_store_b128(u, slot, off + (i * 4 + g) * 1024, 0, kCoherent);
-            }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        int32_t *arrived = (int32_t *)lds;  // (nobody reads the ring any more)
-        if (threadIdx.x == 0)
-            *arrived = __hip_atomic_fetch_add(a.counters + tile, 1, __ATOMIC_ACQ_REL,
-                                              __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        if (*arrived != a.parts - 1)
-            return;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-            acc[i][0] = f32x16{};
-        for (int p = 0; p < a.parts; ++p) {
-            const __amdgpu_buffer_rsrc_t from = make_rsrc(a.partials + ((int64_t)p * tiles + tile) * kSlot);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const f32x4 v = __builtin_bit_cast(
-                        f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, off + (i * 4 + g) * 1024, 0,
-                                                                     kCoherent));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][0][4 * g + e] += v[e];
-                }
-        }
-    }
+    if (a.parts == 1 || !shared)
+        add_adapters<DT, 32 * MT, MT, 1>(acc, a, lds, m0, 0, n0 + wave * 32,
+                                         shared ? 0 : part - a.k_parts,
+                                         shared ? 1 : a.parts - a.k_parts);
+    if (a.parts > 1 && !join_parts(acc, a, lds, part, tm * a.tiles_n + tn))
+        return;
     const __amdgpu_buffer_rsrc_t c = c_rows(a, m0);
     const bool vec = a.c_vec || n0 + kNarrow <= a.N;
 #pragma unroll
@@ -479,18 +658,28 @@ __global__ __launch_bounds__(256, 2) void adapter_narrow_kernel(AdapterArgs a)
 template <bool W_KC>
 __global__ __launch_bounds__(kXThreads) void adapter_exact_kernel(AdapterArgs a)
 {
-    __shared__ __attribute__((aligned(16))) float lds[4 * kXDeep * kXPitch];
+    constexpr int kRings = 4 * kXDeep * kXPitch * 4, kAdapters = adapters_lds<0, kXTile, 2>();
+    __shared__ __attribute__((aligned(16))) float lds[(kRings > kAdapters ? kRings : kAdapters) / 4];
     int tm, tn;
     if (!find_tile(a, (int)blockIdx.x, &tm, &tn))
         return;
-    const int m0 = tm * kXTile, n0 = tn * kXTile;
+    const int m0 = tm * kXTile, n0 = tn * kXTile, part = (int)blockIdx.y;
     const int m = a.rows - m0 < kXTile ? a.rows - m0 : kXTile;
+    const bool shared = part < a.k_parts;
+    const int k0 = shared ? part * a.part_k : 0;
+    const int k = !shared ? 0 : (a.K - k0 < a.part_k ? a.K - k0 : a.part_k);
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     f32x16 acc[2][2];
-    exact_tile<float, true, W_KC>(acc, lds, (const float *)a.X + (int64_t)m0 * a.ldx, a.ldx, m,
-                                  (const float *)a.W + (W_KC ? (int64_t)n0 * a.ldw : n0), a.ldw,
-                                  a.N - n0, a.K);
-    add_adapters<0, 2, 2>(acc, a, m0 + (wave >> 1) * 64, n0 + (wave & 1) * 64, 0, 1);
+    exact_tile<true, W_KC>(acc, lds, (const float *)a.X + (int64_t)m0 * a.ldx + k0, a.ldx, m,
+                           (const float *)a.W + (W_KC ? (int64_t)n0 * a.ldw + k0
+                                                      : (int64_t)k0 * a.ldw + n0),
+                           a.ldw, a.N - n0, k);
+    if (a.parts == 1 || !shared)
+        add_adapters<0, kXTile, 2, 2>(acc, a, (uint8_t *)lds, m0, (wave >> 1) * 64,
+                                      n0 + (wave & 1) * 64, shared ? 0 : part - a.k_parts,
+                                      shared ? 1 : a.parts - a.k_parts);
+    if (a.parts > 1 && !join_parts(acc, a, (uint8_t *)lds, part, tm * a.tiles_n + tn))
+        return;
     store_exact(acc, a.C + (int64_t)m0 * c_row_bytes(a), a.N, m, n0, a.N, a.c_dtype, a.c_vec);
 }
 
@@ -541,7 +730,7 @@ int check(const gemm_adapter *p)
 struct AdapterPlan {
     int mt;                  // few-rows tiles of 32 mt x 128; 0: 256x256 (fp32: 128x128)
     int64_t tiles_m, tiles_n;
-    int parts, part_k, slices, slice_k, rank_pad;
+    int parts, part_k, k_parts, rb, slices, slice_k, rank_pad;
     int64_t ldx, ldw, w_rows, w_cols;
     bool pack_x, pack_w;
     size_t off_h, off_counters, off_partials, off_x, off_w, bytes;
@@ -562,25 +751,34 @@ AdapterPlan plan(const gemm_adapter *p)
     if (E == 2) {
         // 256x256 tiles once they can occupy half the chip
         const int64_t big = cdiv(p->rows, kBig) * cdiv(p->N, kBig);
-        l.mt = big >= kCus / 2 ? 0 : (p->rows <= 32 ? 1 : (p->rows <= 64 ? 2 : 4));
+        l.mt = big >= kCus / 2 ? 0
+               : (p->rows <= 32 ? 1 : (cdiv(p->rows, 64) * cdiv(p->N, kNarrow) <= 2 * kCus ? 2 : 4));
         bm = l.mt ? 32 * l.mt : kBig;
         bn = l.mt ? kNarrow : kBig;
     }
     l.tiles_m = cdiv(p->rows, bm);
     l.tiles_n = cdiv(p->N, bn);
     l.parts = 1;
-    if (l.mt) {
-        // two workgroups per CU, each at least four slabs deep
-        const int64_t want = 2 * kCus / (l.tiles_m * l.tiles_n > 0 ? l.tiles_m * l.tiles_n : 1);
+    if (l.mt || E == 4) {
+        // the depth over half the CUs (fp32, bound by its products: over all),
+        // each part at least 256 deep
+        const int64_t want =
+            (E == 4 ? kCus : kCus / 2) / (l.tiles_m * l.tiles_n > 0 ? l.tiles_m * l.tiles_n : 1);
         const int64_t most = p->K / 256 > 0 ? p->K / 256 : 1;
         l.parts = (int)(want < 1 ? 1 : (want < most ? want : most));
     }
     l.part_k = (int)(cdiv(cdiv(p->K, l.parts), 64) * 64);
     l.parts = l.part_k ? (int)cdiv(p->K, l.part_k) : 1;
-    const int64_t blocks = cdiv(p->rows, kShrinkRows);
-    int64_t slices = blocks ? 128 / blocks : 1;
-    slices = slices < 1 ? 1 : (slices > 16 ? 16 : slices);
-    const int64_t most = p->K / 256 > 0 ? p->K / 256 : 1;
+    l.k_parts = l.parts;
+    if (l.parts > 1)
+        l.parts *= 2;  // the adapters over the other half
+    // the rank projection: blocks of 16 rows while they are few, and slices to
+    // a workgroup per CU, each at least 128 deep
+    l.rb = p->rows <= 512 ? 1 : 2;
+    const int64_t blocks = cdiv(p->rows, 16 * l.rb);
+    int64_t slices = blocks ? kCus / blocks : 1;
+    slices = slices < 1 ? 1 : (slices > 32 ? 32 : slices);
+    const int64_t most = p->K / 128 > 0 ? p->K / 128 : 1;
     slices = slices < most ? slices : most;
     l.slice_k = (int)(cdiv(cdiv(p->K, slices), 32) * 32);
     l.slices = l.slice_k ? (int)cdiv(p->K, l.slice_k) : 1;
@@ -603,18 +801,30 @@ AdapterPlan plan(const gemm_adapter *p)
     return l;
 }
 
-template <int DT>
-void launch_shrink(const AdapterArgs &a, dim3 grid, hipStream_t s)
+template <int DT, int RB>
+void launch_shrink(const AdapterArgs &a, hipStream_t s)
 {
-    const dim3 t(64 * kShrinkWaves);
+    const dim3 grid((unsigned)cdiv(a.rows, 16 * RB), (unsigned)a.slices);
+#define GSK_SHRINK(RT)                                                                           \
+    hipLaunchKernelGGL((shrink_kernel<DT, RT, RB>), grid, dim3(64 * shrink_waves(RT, RB)), 0, s, a)
     if (a.rank <= 16)
-        hipLaunchKernelGGL((shrink_kernel<DT, 1>), grid, t, 0, s, a);
+        GSK_SHRINK(1);
     else if (a.rank <= 32)
-        hipLaunchKernelGGL((shrink_kernel<DT, 2>), grid, t, 0, s, a);
+        GSK_SHRINK(2);
     else if (a.rank <= 64)
-        hipLaunchKernelGGL((shrink_kernel<DT, 4>), grid, t, 0, s, a);
+        GSK_SHRINK(4);
     else
-        hipLaunchKernelGGL((shrink_kernel<DT, 8>), grid, t, 0, s, a);
+        GSK_SHRINK(8);
+#undef GSK_SHRINK
+}
+
+template <int DT>
+void launch_shrink(const AdapterArgs &a, int rb, hipStream_t s)
+{
+    if (rb == 1)
+        launch_shrink<DT, 1>(a, s);
+    else
+        launch_shrink<DT, 2>(a, s);
 }
 
 template <int DT, int LB>
@@ -692,6 +902,7 @@ int gemm_adapter_run(const gemm_adapter *p, const void *X, const void *W, const 
     a.slice_k = l.slice_k;
     a.parts = l.parts;
     a.part_k = l.part_k;
+    a.k_parts = l.k_parts;
     a.terms = p->dtype == GEMM_BF16 && c_dtype == GEMM_F32 ? 3 : 2;
     a.tiles_m = (int32_t)l.tiles_m;
     a.tiles_n = (int32_t)l.tiles_n;
@@ -715,23 +926,22 @@ int gemm_adapter_run(const gemm_adapter *p, const void *X, const void *W, const 
         if (l.pack_w)
             a.W = ws + l.off_w;
     }
-    const dim3 shrink((unsigned)cdiv(p->rows, kShrinkRows), (unsigned)l.slices);
     if (p->dtype == GEMM_F32) {
-        launch_shrink<0>(a, shrink, s);
+        launch_shrink<0>(a, l.rb, s);
         if (p->w_transposed)
-            hipLaunchKernelGGL((adapter_exact_kernel<true>), dim3((unsigned)tiles), dim3(kXThreads),
-                               0, s, a);
+            hipLaunchKernelGGL((adapter_exact_kernel<true>), dim3((unsigned)tiles, (unsigned)a.parts),
+                               dim3(kXThreads), 0, s, a);
         else
-            hipLaunchKernelGGL((adapter_exact_kernel<false>), dim3((unsigned)tiles), dim3(kXThreads),
-                               0, s, a);
+            hipLaunchKernelGGL((adapter_exact_kernel<false>), dim3((unsigned)tiles, (unsigned)a.parts),
+                               dim3(kXThreads), 0, s, a);
     } else if (p->dtype == GEMM_F16) {
-        launch_shrink<1>(a, shrink, s);
+        launch_shrink<1>(a, l.rb, s);
         if (p->w_transposed)
             launch_shared<1, LINES>(a, l.mt, (unsigned)tiles, s);
         else
             launch_shared<1, KROWS>(a, l.mt, (unsigned)tiles, s);
     } else {
-        launch_shrink<2>(a, shrink, s);
+        launch_shrink<2>(a, l.rb, s);
         if (p->w_transposed)
             launch_shared<2, LINES>(a, l.mt, (unsigned)tiles, s);
         else

@@ -10,6 +10,7 @@ namespace dev {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -122,6 +123,12 @@ __device__ __forceinline__ void barrier_only()
     // keeps the compiler from moving LDS accesses across it
     asm volatile("s_barrier" ::: "memory");
 }
+
+// A compile-time index as an argument.
+template <int V>
+struct IC {
+    static constexpr int value = V;
+};
 
 template <int N>
 __device__ __forceinline__ void wait_vmcnt()

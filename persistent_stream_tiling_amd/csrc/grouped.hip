@@ -18,41 +18,6 @@ using namespace dev;
 
 namespace {
 
-template <typename T, bool B_KC>
-__global__ __launch_bounds__(kXThreads) void rows_exact_kernel(GroupedArgs a)
-{
-    __shared__ __attribute__((aligned(16))) float lds[4 * kXDeep * kXPitch];
-    RowTile t;
-    if (!find_row_tile<kXTile>(a, blockIdx.x, &t))
-        return;
-    const int n0 = t.tn * kXTile, m = t.m_end - t.m0 < kXTile ? t.m_end - t.m0 : kXTile;
-    const T *A = (const T *)a.A + (int64_t)t.m0 * a.lda;
-    // (the rows past the last group multiply nothing: depth 0)
-    const T *B = (const T *)a.B + (t.g < a.groups ? t.g * a.b_stride : 0) +
-                 (B_KC ? (int64_t)n0 * a.ldb : n0);
-    f32x16 acc[2][2];
-    exact_tile<T, true, B_KC>(acc, lds, A, a.lda, m, B, a.ldb, a.N - n0, t.g < a.groups ? a.K : 0);
-    store_exact(acc, a.C + (int64_t)t.m0 * a.N * (a.c_dtype ? 2 : 4), a.N, m, n0, a.N, a.c_dtype,
-                a.c_vec);
-}
-
-template <typename T>
-__global__ __launch_bounds__(kXThreads) void wgrad_exact_kernel(GroupedArgs a)
-{
-    __shared__ __attribute__((aligned(16))) float lds[4 * kXDeep * kXPitch];
-    const int64_t per = (int64_t)a.tiles_m * a.tiles_n;
-    const int32_t g = (int32_t)(blockIdx.x / per);
-    const int32_t in = (int32_t)(blockIdx.x - g * per);
-    const int m0 = in / a.tiles_n * kXTile, n0 = in % a.tiles_n * kXTile;
-    int32_t lo, hi;
-    group_rows(a.offsets, g, a.groups, a.rows, &lo, &hi);
-    f32x16 acc[2][2];
-    exact_tile<T, false, false>(acc, lds, (const T *)a.A + (int64_t)lo * a.lda + m0, a.lda, a.M - m0,
-                                (const T *)a.B + (int64_t)lo * a.ldb + n0, a.ldb, a.N - n0, hi - lo);
-    store_exact(acc, a.C + ((int64_t)g * a.M + m0) * a.N * (a.c_dtype ? 2 : 4), a.N, a.M - m0, n0,
-                a.N, a.c_dtype, a.c_vec);
-}
-
 __device__ __forceinline__ uint32_t c_row_bytes(const GroupedArgs &a)
 {
     return (uint32_t)a.N * (a.c_dtype ? 2 : 4);
@@ -62,6 +27,39 @@ __device__ __forceinline__ uint32_t c_row_bytes(const GroupedArgs &a)
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t c_rows(const GroupedArgs &a, int64_t row)
 {
     return make_rsrc(a.C + row * c_row_bytes(a));
+}
+
+template <bool B_KC>
+__global__ __launch_bounds__(kXThreads, 2) void rows_exact_kernel(GroupedArgs a)
+{
+    __shared__ __attribute__((aligned(16))) float lds[4 * kXDeep * kXPitch];
+    RowTile t;
+    if (!find_row_tile<kXTile>(a, blockIdx.x, &t))
+        return;
+    const int n0 = t.tn * kXTile, m = t.m_end - t.m0 < kXTile ? t.m_end - t.m0 : kXTile;
+    // (the rows past the last group multiply nothing: depth 0)
+    const float *B = (const float *)a.B + (t.g < a.groups ? t.g * a.b_stride : 0) +
+                     (B_KC ? (int64_t)n0 * a.ldb : n0);
+    f32x16 acc[2][2];
+    exact_tile<true, B_KC>(acc, lds, (const float *)a.A + (int64_t)t.m0 * a.lda, a.lda, m, B, a.ldb,
+                           a.N - n0, t.g < a.groups ? a.K : 0);
+    store_exact(acc, a.C + (int64_t)t.m0 * c_row_bytes(a), a.N, m, n0, a.N, a.c_dtype, a.c_vec);
+}
+
+__global__ __launch_bounds__(kXThreads, 2) void wgrad_exact_kernel(GroupedArgs a)
+{
+    __shared__ __attribute__((aligned(16))) float lds[4 * kXDeep * kXPitch];
+    const int64_t per = (int64_t)a.tiles_m * a.tiles_n;
+    const int32_t g = (int32_t)(blockIdx.x / per);
+    const int32_t in = (int32_t)(blockIdx.x - g * per);
+    const int m0 = in / a.tiles_n * kXTile, n0 = in % a.tiles_n * kXTile;
+    int32_t lo, hi;
+    group_rows(a.offsets, g, a.groups, a.rows, &lo, &hi);
+    f32x16 acc[2][2];
+    exact_tile<false, false>(acc, lds, (const float *)a.A + (int64_t)lo * a.lda + m0, a.lda, a.M - m0,
+                             (const float *)a.B + (int64_t)lo * a.ldb + n0, a.ldb, a.N - n0, hi - lo);
+    store_exact(acc, a.C + ((int64_t)g * a.M + m0) * c_row_bytes(a), a.N, a.M - m0, n0, a.N,
+                a.c_dtype, a.c_vec);
 }
 
 // Row tile t by the columns from n0 on.  The rows past the last group
@@ -83,7 +81,7 @@ __device__ __forceinline__ TileWork rows_work(const GroupedArgs &a, const RowTil
 template <int DT, int LB>
 __global__ __launch_bounds__(512, 1) void rows_big_kernel(GroupedArgs a)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[(ring_of(LINES) + ring_of(LB)) * kPiece];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[(ring_of(0, LINES) + ring_of(1, LB)) * kPiece];
     RowTile t;
     if (!find_row_tile<kBig>(a, blockIdx.x, &t))
         return;
@@ -91,9 +89,9 @@ __global__ __launch_bounds__(512, 1) void rows_big_kernel(GroupedArgs a)
     const TileWork w = rows_work<LB>(a, t, n0);
     const __amdgpu_buffer_rsrc_t c = c_rows(a, t.m0);
     const bool vec = a.c_vec || n0 + kBig <= a.N;
-    big_tile<DT, LINES, LB>(w, lds, [&](const f32x16 (&acc)[4][2], int row, int col) {
+    big_tile<DT, LINES, LB>(w, lds, [&](const f32x16 (&acc)[4][2], auto blocks, int row, int col) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 2 * decltype(blocks)::value; ++i)
             store_block(acc[i >> 1][i & 1], c, c_row_bytes(a), row + (i >> 1) * 32, w.m,
                         n0 + col + (i & 1) * 32, a.N, vec, a.c_dtype);
     });
@@ -121,7 +119,7 @@ __global__ __launch_bounds__(256, 2) void rows_narrow_kernel(GroupedArgs a)
 template <int DT>
 __global__ __launch_bounds__(512, 1) void wgrad_big_kernel(GroupedArgs a)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * ring_of(KROWS) * kPiece];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[(ring_of(0, KROWS) + ring_of(1, KROWS)) * kPiece];
     const int64_t per = (int64_t)a.tiles_m * a.tiles_n;
     const int32_t g = (int32_t)(blockIdx.x / per);
     const int32_t in = (int32_t)(blockIdx.x - g * per);
@@ -138,9 +136,9 @@ __global__ __launch_bounds__(512, 1) void wgrad_big_kernel(GroupedArgs a)
     w.k = hi - lo;
     const __amdgpu_buffer_rsrc_t c = c_rows(a, (int64_t)g * a.M + m0);
     const bool vec = a.c_vec || n0 + kBig <= a.N;
-    big_tile<DT, KROWS, KROWS>(w, lds, [&](const f32x16 (&acc)[4][2], int row, int col) {
+    big_tile<DT, KROWS, KROWS>(w, lds, [&](const f32x16 (&acc)[4][2], auto blocks, int row, int col) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 2 * decltype(blocks)::value; ++i)
             store_block(acc[i >> 1][i & 1], c, c_row_bytes(a), row + (i >> 1) * 32, w.m,
                         n0 + col + (i & 1) * 32, a.N, vec, a.c_dtype);
     });
@@ -347,11 +345,11 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
     } while (0)
     if (E == 4) {
         if (wgrad)
-            GSK_GROUPED(wgrad_exact_kernel, float);
+            hipLaunchKernelGGL(wgrad_exact_kernel, dim3((unsigned)tiles), dim3(threads), 0, s, a);
         else if (bt)
-            GSK_GROUPED(rows_exact_kernel, float, true);
+            GSK_GROUPED(rows_exact_kernel, true);
         else
-            GSK_GROUPED(rows_exact_kernel, float, false);
+            GSK_GROUPED(rows_exact_kernel, false);
     } else if (p->dtype == GEMM_F16) {
         GSK_GROUPED_16(1);
     } else {

@@ -18,6 +18,8 @@
 namespace gsk {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 // ------------------------------------------------------------------ the sort
 
 constexpr int kRouteThreads = 1024;
@@ -209,50 +211,68 @@ int launch_route(const Id *ids, int64_t entries, int groups, int32_t *offsets, i
 constexpr int kRowThreads = 256;
 constexpr int kRowMaxBlocks = 1 << 16;  // further tokens go round again (a launch holds 2^32 threads)
 
-// 16 bytes of a row whose start is only element-aligned (rows need not be
-// whole 16-byte words): gfx950 code runs with unaligned global access enabled,
-// so this is one 16-byte access.
+// 16 bytes of a row.  Rows need not be whole 16-byte words, so they start at
+// any element: gfx950 code runs with unaligned global access enabled, and a
+// 16-byte copy to or from an element-aligned address is one access.  (The
+// values stay whole vectors from load to store: as arrays of elements they
+// were moved two bytes at a time.)
 template <typename T>
 struct Row16 {
     static constexpr int V = 16 / (int)sizeof(T);
-    struct __attribute__((packed, aligned(sizeof(T)))) Words {
-        uint32_t w[4];
-    };
+    typedef T Elements __attribute__((ext_vector_type(16 / sizeof(T))));
 };
 
+// The elements of a row from column c, those past `cols` as zero.
 template <typename T>
-__device__ __forceinline__ float to_f32(T x)
+__device__ __forceinline__ u32x4 load_vec(const T *row, int c, int cols)
 {
-    return (float)x;
-}
-
-// V elements of a row from column c, those past `cols` as zero.
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(T (&x)[V], const T *row, int c, int cols)
-{
+    constexpr int V = Row16<T>::V;
+    u32x4 w;
     if (c + V <= cols) {
-        const auto w = *(const typename Row16<T>::Words *)(row + c);
-        __builtin_memcpy(x, &w, 16);
+        __builtin_memcpy(&w, row + c, 16);
     } else {
+        T x[V];
 #pragma unroll
         for (int e = 0; e < V; ++e)
             x[e] = c + e < cols ? row[c + e] : (T)0.0f;
+        __builtin_memcpy(&w, x, 16);
     }
+    return w;
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T *row, int c, int cols, const T (&x)[V])
+template <typename T>
+__device__ __forceinline__ void store_vec(T *row, int c, int cols, u32x4 w)
 {
+    constexpr int V = Row16<T>::V;
     if (c + V <= cols) {
-        typename Row16<T>::Words w;
-        __builtin_memcpy(&w, x, 16);
-        *(typename Row16<T>::Words *)(row + c) = w;
+        __builtin_memcpy(row + c, &w, 16);
     } else {
+        T x[V];
+        __builtin_memcpy(x, &w, 16);
 #pragma unroll
         for (int e = 0; e < V; ++e)
             if (c + e < cols)
                 row[c + e] = x[e];
     }
+}
+
+template <typename T>
+__device__ __forceinline__ void widen(float (&x)[Row16<T>::V], u32x4 w)
+{
+    const auto v = __builtin_bit_cast(typename Row16<T>::Elements, w);
+#pragma unroll
+    for (int e = 0; e < Row16<T>::V; ++e)
+        x[e] = (float)v[e];
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 narrow(const float (&x)[Row16<T>::V])
+{
+    typename Row16<T>::Elements v;
+#pragma unroll
+    for (int e = 0; e < Row16<T>::V; ++e)
+        v[e] = (T)x[e];
+    return __builtin_bit_cast(u32x4, v);
 }
 
 // How a workgroup covers rows: `lanes` threads (a power of two) per token and
@@ -270,10 +290,24 @@ __device__ __forceinline__ int64_t rows_kept(const int32_t *kept, int64_t entrie
     return n < 0 ? 0 : (n < entries ? n : entries);
 }
 
+// Sorted rows of choices j0 .. j0 + J - 1 of token t (-1: dropped, or past the
+// last choice).  All J loads are in flight at once.
+template <int J>
+__device__ __forceinline__ void load_rows(int32_t (&row)[J], const int32_t *position, int64_t e0,
+                                          int j0, int choices, int64_t entries)
+{
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        row[j] = position[e0 + (j0 + j < choices ? j0 + j : 0)];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        row[j] = j0 + j < choices && row[j] < entries ? row[j] : -1;
+}
+
 // xs[position[t][j]] = x[t] for every choice j; rows past the kept ones are
 // zeroed (row e = t * choices + j by token t: rows and entries count alike).
-// Bound by the writes, choices rows for each row read.
-template <typename T>
+// J: choices per round.  Bound by the writes, choices rows for each row read.
+template <typename T, int J>
 __global__ __launch_bounds__(kRowThreads) void gather_kernel(const T *__restrict__ x,
                                                              const int32_t *__restrict__ position,
                                                              const int32_t *__restrict__ kept,
@@ -285,32 +319,29 @@ __global__ __launch_bounds__(kRowThreads) void gather_kernel(const T *__restrict
     const int c = ((int)blockIdx.y * lanes + (threadIdx.x & (lanes - 1))) * V;
     if (c >= g.cols)
         return;
-    T zero[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-        zero[e] = (T)0.0f;
     for (int64_t t = (int64_t)blockIdx.x * per + (threadIdx.x >> g.lanes_log2); t < g.tokens;
          t += (int64_t)gridDim.x * per) {
-        T v[V];
-        load_vec<T, V>(v, x + t * g.cols, c, g.cols);
+        const u32x4 v = load_vec(x + t * g.cols, c, g.cols);
         const int64_t e0 = t * g.choices;
-        for (int j = 0; j < g.choices; ++j) {
-            const int32_t row = position[e0 + j];
-            if (row >= 0 && row < entries)
-                store_vec<T, V>(xs + (int64_t)row * g.cols, c, g.cols, v);
-            if (e0 + j >= live)
-                store_vec<T, V>(xs + (e0 + j) * g.cols, c, g.cols, zero);
+        for (int j0 = 0; j0 < g.choices; j0 += J) {
+            int32_t row[J];
+            load_rows<J>(row, position, e0, j0, g.choices, entries);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (row[j] >= 0)
+                    store_vec(xs + (int64_t)row[j] * g.cols, c, g.cols, v);
         }
+        for (int64_t e = e0 > live ? e0 : live; e < e0 + g.choices; ++e)
+            store_vec(xs + e * g.cols, c, g.cols, u32x4{});
     }
 }
 
-constexpr int kBatch = 8;  // choices whose rows are in flight at once
-
 // y[t] = sum over j of w[t][j] * ys[position[t][j]], in fp32 in the order of
-// j, rounded once.  A dropped choice's row is not read.  Without weights: the
-// plain sum, which is the gradient of gather_kernel.  Bound by the reads of
-// the sorted rows; eight rows' loads are in flight per thread.
-template <typename T, bool WEIGHTS>
+// j, rounded once.  A dropped choice adds nothing (its loads go to row 0, so
+// that all J of a round are in flight together, and are then ignored).
+// Without weights: the plain sum, which is the gradient of gather_kernel.
+// Bound by the reads of the sorted rows.
+template <typename T, bool WEIGHTS, int J>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(const T *__restrict__ ys,
                                                               const int32_t *__restrict__ position,
                                                               const float *__restrict__ weights,
@@ -324,36 +355,31 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(const T *__restric
         return;
     for (int64_t t = (int64_t)blockIdx.x * per + (threadIdx.x >> g.lanes_log2); t < g.tokens;
          t += (int64_t)gridDim.x * per) {
+        const int64_t e0 = t * g.choices;
         float sum[V] = {};
-        for (int j0 = 0; j0 < g.choices; j0 += kBatch) {
-            int32_t row[kBatch];
-            float w[kBatch];
-            T v[kBatch][V];
+        for (int j0 = 0; j0 < g.choices; j0 += J) {
+            int32_t row[J];
+            float w[J];
+            u32x4 v[J];
+            load_rows<J>(row, position, e0, j0, g.choices, entries);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const bool in = j0 + j < g.choices;
-                const int64_t e = t * g.choices + (in ? j0 + j : 0);
-                row[j] = in ? position[e] : -1;
-                row[j] = row[j] < entries ? row[j] : -1;
-                w[j] = WEIGHTS ? weights[e] : 1.0f;
+            for (int j = 0; j < J; ++j)
+                w[j] = WEIGHTS ? weights[e0 + (j0 + j < g.choices ? j0 + j : 0)] : 1.0f;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                v[j] = load_vec(ys + (int64_t)(row[j] >= 0 ? row[j] : 0) * g.cols, c, g.cols);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                float x[V];
+                widen<T>(x, v[j]);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float next = WEIGHTS ? __builtin_fmaf(w[j], x[e], sum[e]) : sum[e] + x[e];
+                    sum[e] = row[j] >= 0 ? next : sum[e];
+                }
             }
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if (row[j] >= 0)
-                    load_vec<T, V>(v[j], ys + (int64_t)row[j] * g.cols, c, g.cols);
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if (row[j] >= 0)
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        sum[e] = WEIGHTS ? __builtin_fmaf(w[j], to_f32(v[j][e]), sum[e])
-                                         : sum[e] + to_f32(v[j][e]);
         }
-        T out[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            out[e] = (T)sum[e];
-        store_vec<T, V>(y + t * g.cols, c, g.cols, out);
+        store_vec(y + t * g.cols, c, g.cols, narrow<T>(sum));
     }
 }
 
@@ -361,14 +387,15 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(const T *__restric
 // dw[t][j] = <dy[t], ys[position[t][j]]> (zero for a dropped choice), in one
 // pass over ys; rows of dys past the kept ones are zeroed.  The dot products
 // are summed per lane over its columns, then over the lanes in a fixed order.
-template <typename T>
+// U: column steps whose loads are in flight together.
+template <typename T, int J, int U>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(
     const T *__restrict__ dy, const T *__restrict__ ys, const int32_t *__restrict__ position,
     const int32_t *__restrict__ kept, const float *__restrict__ weights, T *__restrict__ dys,
     float *__restrict__ dweights, RowGrid g)
 {
     constexpr int V = Row16<T>::V;
-    __shared__ float part[kRowThreads / 64][kBatch];
+    __shared__ float part[kRowThreads / 64][J];
     const int lanes = 1 << g.lanes_log2, per = kRowThreads >> g.lanes_log2;
     const int l = threadIdx.x & (lanes - 1), wave = threadIdx.x >> 6;
     const int64_t entries = g.tokens * g.choices, live = rows_kept(kept, entries);
@@ -378,61 +405,66 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(
         const bool ok = t < g.tokens;
         const int64_t e0 = ok ? t * g.choices : 0;
         const T *dy_row = dy + (ok ? t : 0) * g.cols;
-        for (int j0 = 0; j0 < g.choices; j0 += kBatch) {
-            int32_t row[kBatch];
-            float w[kBatch], dot[kBatch];
+        const int cols = ok ? g.cols : 0;
+        for (int j0 = 0; j0 < g.choices; j0 += J) {
+            int32_t row[J];
+            float w[J], dot[J];
+            load_rows<J>(row, position, e0, j0, g.choices, entries);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const bool in = ok && j0 + j < g.choices;
-                const int64_t e = e0 + (in ? j0 + j : 0);
-                row[j] = in ? position[e] : -1;
-                row[j] = row[j] < entries ? row[j] : -1;
-                w[j] = in ? weights[e] : 0.0f;
+            for (int j = 0; j < J; ++j) {
+                w[j] = weights[e0 + (j0 + j < g.choices ? j0 + j : 0)];
                 dot[j] = 0.0f;
             }
-            for (int c = l * V; c < (ok ? g.cols : 0); c += lanes * V) {
-                T d[V], v[kBatch][V];
-                load_vec<T, V>(d, dy_row, c, g.cols);
+            for (int c0 = l * V; c0 < cols; c0 += U * lanes * V) {
+                u32x4 d[U], v[U][J];
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j)
-                    if (row[j] >= 0)
-                        load_vec<T, V>(v[j], ys + (int64_t)row[j] * g.cols, c, g.cols);
+                for (int u = 0; u < U; ++u) {
+                    const int c = c0 + u * lanes * V;
+                    if (c < cols) {
+                        d[u] = load_vec(dy_row, c, cols);
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    if (row[j] >= 0) {
-                        T out[V];
-#pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            dot[j] = __builtin_fmaf(to_f32(d[e]), to_f32(v[j][e]), dot[j]);
-                            out[e] = (T)(w[j] * to_f32(d[e]));
-                        }
-                        store_vec<T, V>(dys + (int64_t)row[j] * g.cols, c, g.cols, out);
+                        for (int j = 0; j < J; ++j)
+                            v[u][j] = load_vec(ys + (int64_t)(row[j] >= 0 ? row[j] : 0) * cols, c,
+                                               cols);
                     }
-                    if (j0 + j < g.choices && e0 + j0 + j >= live) {
-                        T zero[V];
+                }
 #pragma unroll
-                        for (int e = 0; e < V; ++e)
-                            zero[e] = (T)0.0f;
-                        store_vec<T, V>(dys + (e0 + j0 + j) * g.cols, c, g.cols, zero);
+                for (int u = 0; u < U; ++u) {
+                    const int c = c0 + u * lanes * V;
+                    if (c < cols) {
+                        float df[V];
+                        widen<T>(df, d[u]);
+#pragma unroll
+                        for (int j = 0; j < J; ++j) {
+                            float vf[V], out[V];
+                            widen<T>(vf, v[u][j]);
+#pragma unroll
+                            for (int e = 0; e < V; ++e) {
+                                dot[j] = __builtin_fmaf(df[e], vf[e], dot[j]);
+                                out[e] = w[j] * df[e];
+                            }
+                            if (row[j] >= 0)
+                                store_vec(dys + (int64_t)row[j] * cols, c, cols, narrow<T>(out));
+                        }
                     }
                 }
             }
             // over the token's lanes: within the wave, then over its waves
             const int width = lanes < 64 ? lanes : 64;
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j)
+            for (int j = 0; j < J; ++j)
                 for (int d = width >> 1; d; d >>= 1)
                     dot[j] += __shfl_xor(dot[j], d);
             if (lanes > 64) {
                 __syncthreads();
                 if ((threadIdx.x & 63) == 0)
 #pragma unroll
-                    for (int j = 0; j < kBatch; ++j)
+                    for (int j = 0; j < J; ++j)
                         part[wave][j] = dot[j];
                 __syncthreads();
                 const int w0 = (threadIdx.x >> g.lanes_log2) * (lanes >> 6);
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
+                for (int j = 0; j < J; ++j) {
                     dot[j] = part[w0][j];
                     for (int i = 1; i < lanes >> 6; ++i)
                         dot[j] += part[w0 + i][j];
@@ -440,9 +472,14 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(
             }
             if (ok && l == 0)
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j)
+                for (int j = 0; j < J; ++j)
                     if (j0 + j < g.choices)
                         dweights[e0 + j0 + j] = row[j] >= 0 ? dot[j] : 0.0f;
+        }
+        if (ok && e0 + g.choices > live) {
+            for (int64_t e = e0 > live ? e0 : live; e < e0 + g.choices; ++e)
+                for (int c = l * V; c < g.cols; c += lanes * V)
+                    store_vec(dys + e * g.cols, c, g.cols, u32x4{});
         }
     }
 }
@@ -504,6 +541,19 @@ int check_rows(int64_t tokens, int32_t choices, int64_t cols, int dtype)
 }
 
 bool aligned(const void *p, int n) { return ((uintptr_t)p & (uintptr_t)(n - 1)) == 0; }
+
+// One of the kernels for 1, 2, 4 or 8 choices a round: LAUNCH(T, J).
+#define GSK_BY_CHOICES(LAUNCH, T)                                                                \
+    do {                                                                                         \
+        if (choices == 1)                                                                        \
+            LAUNCH(T, 1);                                                                        \
+        else if (choices == 2)                                                                   \
+            LAUNCH(T, 2);                                                                        \
+        else if (choices <= 4)                                                                   \
+            LAUNCH(T, 4);                                                                        \
+        else                                                                                     \
+            LAUNCH(T, 8);                                                                        \
+    } while (0)
 
 }  // namespace
 }  // namespace gsk
@@ -577,13 +627,14 @@ int gemm_gather_rows(const void *x, const int32_t *position, const int32_t *kept
     const RowGrid g = row_grid(tokens, choices, (int32_t)cols, E);
     const dim3 blocks = row_blocks(g, E, true);
     // a copy: only the element size matters
+#define GSK_GATHER(T, J)                                                                         \
+    hipLaunchKernelGGL((gather_kernel<T, J>), blocks, dim3(kRowThreads), 0, (hipStream_t)stream, \
+                       (const T *)x, position, kept, (T *)xs, g)
     if (E == 4)
-        hipLaunchKernelGGL((gather_kernel<float>), blocks, dim3(kRowThreads), 0,
-                           (hipStream_t)stream, (const float *)x, position, kept, (float *)xs, g);
+        GSK_BY_CHOICES(GSK_GATHER, float);
     else
-        hipLaunchKernelGGL((gather_kernel<_Float16>), blocks, dim3(kRowThreads), 0,
-                           (hipStream_t)stream, (const _Float16 *)x, position, kept,
-                           (_Float16 *)xs, g);
+        GSK_BY_CHOICES(GSK_GATHER, _Float16);
+#undef GSK_GATHER
     return launched("gather");
 }
 
@@ -605,25 +656,26 @@ int gemm_combine_rows(const void *ys, const int32_t *position, const float *weig
     const RowGrid g = row_grid(tokens, choices, (int32_t)cols, E);
     const dim3 blocks = row_blocks(g, E, true);
     const hipStream_t s = (hipStream_t)stream;
-#define GSK_COMBINE(T, W)                                                                        \
-    hipLaunchKernelGGL((combine_kernel<T, W>), blocks, dim3(kRowThreads), 0, s, (const T *)ys,   \
-                       position, weights, (T *)y, g)
+#define GSK_COMBINE(T, W, J)                                                                     \
+    hipLaunchKernelGGL((combine_kernel<T, W, J>), blocks, dim3(kRowThreads), 0, s,               \
+                       (const T *)ys, position, weights, (T *)y, g)
+#define GSK_WEIGHTED(T, J) GSK_COMBINE(T, true, J)
+#define GSK_PLAIN(T, J) GSK_COMBINE(T, false, J)
+#define GSK_BY_TYPE(T)                                                                           \
+    if (weights)                                                                                 \
+        GSK_BY_CHOICES(GSK_WEIGHTED, T);                                                         \
+    else                                                                                         \
+        GSK_BY_CHOICES(GSK_PLAIN, T)
     if (dtype == GEMM_F32) {
-        if (weights)
-            GSK_COMBINE(float, true);
-        else
-            GSK_COMBINE(float, false);
+        GSK_BY_TYPE(float);
     } else if (dtype == GEMM_F16) {
-        if (weights)
-            GSK_COMBINE(_Float16, true);
-        else
-            GSK_COMBINE(_Float16, false);
+        GSK_BY_TYPE(_Float16);
     } else {
-        if (weights)
-            GSK_COMBINE(__bf16, true);
-        else
-            GSK_COMBINE(__bf16, false);
+        GSK_BY_TYPE(__bf16);
     }
+#undef GSK_BY_TYPE
+#undef GSK_WEIGHTED
+#undef GSK_PLAIN
 #undef GSK_COMBINE
     return launched("combine");
 }
@@ -650,16 +702,16 @@ int gemm_combine_rows_backward(const void *dy, const void *ys, const int32_t *po
     const RowGrid g = row_grid(tokens, choices, (int32_t)cols, E);
     const dim3 blocks = row_blocks(g, E, false);
     const hipStream_t s = (hipStream_t)stream;
-#define GSK_BACK(T)                                                                              \
-    hipLaunchKernelGGL((combine_backward_kernel<T>), blocks, dim3(kRowThreads), 0, s,            \
-                       (const T *)dy, (const T *)ys, position, kept, weights, (T *)dys,          \
-                       dweights, g)
+#define GSK_BACK(T, J)                                                                           \
+    hipLaunchKernelGGL((combine_backward_kernel<T, J, (J > 2 ? 1 : 4 / J)>), blocks,             \
+                       dim3(kRowThreads), 0, s, (const T *)dy, (const T *)ys, position, kept,    \
+                       weights, (T *)dys, dweights, g)
     if (dtype == GEMM_F32)
-        GSK_BACK(float);
+        GSK_BY_CHOICES(GSK_BACK, float);
     else if (dtype == GEMM_F16)
-        GSK_BACK(_Float16);
+        GSK_BY_CHOICES(GSK_BACK, _Float16);
     else
-        GSK_BACK(__bf16);
+        GSK_BY_CHOICES(GSK_BACK, __bf16);
 #undef GSK_BACK
     return launched("combine backward");
 }

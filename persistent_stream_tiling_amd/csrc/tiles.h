@@ -10,113 +10,167 @@ namespace dev {
 // ---------------------------------------------------------------------------
 // fp32: the fp32 matrix instruction, 128x128 tiles, any sizes and alignments.
 //
-// An operand is a slab of 128 rows (m or n) by 16 k per iteration.  It lies in
-// memory either with k contiguous (KC: 8 consecutive k per thread) or with
-// m / n contiguous (8 consecutive m per thread), and in LDS always as
-// [k][m], the order the 32x32x2 instruction reads (lane l: row l % 32, k = l /
-// 32).  LDS rows are 160 floats apart: the two k rows that one read touches
-// are then 32 banks apart.  Two LDS buffers; the next slab's loads are in
-// flight while the current one is multiplied.
-constexpr int kXTile = 128, kXDeep = 16, kXThreads = 256, kXPitch = 160;
+// An operand is a slab of 128 rows (m or n) by 32 k per iteration.  It lies in
+// memory either with k contiguous (KC: eight threads read 128 bytes of a row)
+// or with m / n contiguous (32 threads read 512 bytes of a k-row), four 16-byte
+// loads per thread either way, and in LDS always as [k][m], the order the
+// 32x32x2 instruction reads (lane l: row l % 32, k = l / 32).  LDS rows are 130
+// floats apart, so that the eight k by eight rows that KC threads write at a
+// time fall on 64 banks.  Two LDS buffers, two workgroups per CU; the next
+// slab's loads are in flight while the current one is multiplied.
+constexpr int kXTile = 128, kXDeep = 32, kXThreads = 256, kXPitch = 130;
 
-template <typename T>
-struct Packed8 {
-    struct __attribute__((packed, aligned(sizeof(T)))) Words {
-        uint32_t w[8 * sizeof(T) / 4];
-    };
+struct __attribute__((packed, aligned(4))) Floats4 {
+    float x[4];
 };
 
-// Eight consecutive elements at p, of which the first n (0 .. 8) exist.
-template <typename T>
-__device__ __forceinline__ void load8(float (&x)[8], const T *p, int n)
+// One thread's share of a whole slab of 32 k.  Rows past the last one repeat
+// it, which only gives rows of C that are not stored.
+template <bool KC>
+__device__ __forceinline__ void load_slab(f32x4 (&x)[4], const float *p, int64_t ld, int rows)
 {
-    T t[8];
-    if (n >= 8) {
-        const auto w = *(const typename Packed8<T>::Words *)p;
-        __builtin_memcpy(t, &w, sizeof(t));
-    } else {
+    const int tid = threadIdx.x, last = KC ? rows - 1 : rows - 4;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            t[e] = e < n ? p[e] : (T)0.0f;
+    for (int j = 0; j < 4; ++j) {
+        const int r = KC ? (tid >> 3) + 32 * j : (tid & 31) * 4;
+        const int kk = KC ? (tid & 7) * 4 : (tid >> 5) + 8 * j;
+        const int row = r < last ? r : last;
+        const Floats4 f = *(const Floats4 *)(KC ? p + row * ld + kk : p + kk * ld + row);
+        x[j] = f32x4{f.x[0], f.x[1], f.x[2], f.x[3]};
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        x[e] = (float)t[e];
 }
 
-// One thread's share of a slab: rows [0, rows) x k [0, k) exist at p.
-template <typename T, bool KC>
-__device__ __forceinline__ void load_slab(float (&x)[8], const T *p, int64_t ld, int rows, int k)
+// The same, element by element: rows [0, rows) x k [0, k) exist at p.
+template <bool KC>
+__device__ __forceinline__ void load_part(f32x4 (&x)[4], const float *p, int64_t ld, int rows, int k)
 {
     const int tid = threadIdx.x;
-    const int r = KC ? tid >> 1 : (tid & 15) * 8, kk = KC ? (tid & 1) * 8 : tid >> 4;
-    const int n = KC ? (r < rows ? k - kk : 0) : (kk < k ? rows - r : 0);
-    load8(x, KC ? p + r * ld + kk : p + kk * ld + r, n);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = KC ? (tid >> 3) + 32 * j : (tid & 31) * 4;
+        const int kk = KC ? (tid & 7) * 4 : (tid >> 5) + 8 * j;
+        const int n = KC ? (r < rows ? k - kk : 0) : (kk < k ? rows - r : 0);
+        const float *at = KC ? p + r * ld + kk : p + kk * ld + r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[j][e] = e < n ? at[e] : 0.0f;
+    }
 }
 
 template <bool KC>
-__device__ __forceinline__ void park_slab(float *lds, const float (&x)[8])
+__device__ __forceinline__ void park_slab(float *lds, const f32x4 (&x)[4])
 {
     const int tid = threadIdx.x;
-    if constexpr (KC) {
-        const int r = tid >> 1, kk = (tid & 1) * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            lds[(kk + e) * kXPitch + r] = x[e];
-    } else {
-        float *p = lds + (tid >> 4) * kXPitch + (tid & 15) * 8;
-        *(f32x4 *)p = f32x4{x[0], x[1], x[2], x[3]};
-        *(f32x4 *)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (KC) {
+            float *p = lds + (tid & 7) * 4 * kXPitch + (tid >> 3) + 32 * j;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                p[e * kXPitch] = x[j][e];
+        } else {
+            // (rows are 8-byte aligned)
+            f32x2 *p = (f32x2 *)(lds + ((tid >> 5) + 8 * j) * kXPitch + (tid & 31) * 4);
+            p[0] = f32x2{x[j][0], x[j][1]};
+            p[1] = f32x2{x[j][2], x[j][3]};
+        }
     }
 }
 
 // acc (2 x 2 blocks of 32x32 per wave, 2 x 2 waves) = the tile's sums over k
 // in [0, k).  The operands are swapped in the instruction, so lane l holds
 // C[32*mt + l % 32][32*nt + 8*g + 4*(l / 32) + e] in register 4*g + e.
-template <typename T, bool A_KC, bool B_KC>
-__device__ __forceinline__ void exact_tile(f32x16 (&acc)[2][2], float *lds, const T *a, int64_t lda,
-                                           int m, const T *b, int64_t ldb, int n, int k)
+template <bool A_KC, bool B_KC>
+__device__ __forceinline__ void exact_tile(f32x16 (&acc)[2][2], float *lds, const float *a,
+                                           int64_t lda, int m, const float *b, int64_t ldb, int n,
+                                           int k)
 {
     constexpr int kSlab = kXDeep * kXPitch;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int half = lane >> 5, l32 = lane & 31;
     const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
     const int64_t a_step = A_KC ? kXDeep : kXDeep * lda, b_step = B_KC ? kXDeep : kXDeep * ldb;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         acc[i >> 1][i & 1] = f32x16{};
-    float xa[8], xb[8];
-    if (k > 0) {
-        load_slab<T, A_KC>(xa, a, lda, m, k);
-        load_slab<T, B_KC>(xb, b, ldb, n, k);
+    // (row blocks of the wave that hold no row of the tile are not multiplied)
+    const int blocks = (m - wm + 31) >> 5;
+    const auto multiply_blocks = [&](const float *sa, const float *sb, auto nb) {
+        constexpr int NB = decltype(nb)::value;
+        // four k pairs' operands are read while the four before are multiplied
+        float fa[2][4][2], fb[2][4][2];
+        const auto read_four = [&](int s, int kk) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int row = (kk + 2 * p + half) * kXPitch + l32;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (i < NB)
+                        fa[s][p][i] = sa[row + wm + 32 * i];
+                    fb[s][p][i] = sb[row + wn + 32 * i];
+                }
+            }
+        };
+        read_four(0, 0);
+#pragma unroll
+        for (int kk = 0; kk < kXDeep; kk += 8) {
+            const int s = (kk >> 3) & 1;
+            __builtin_amdgcn_sched_barrier(0);
+            if (kk + 8 < kXDeep)
+                read_four(s ^ 1, kk + 8);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+#pragma unroll
+                for (int i = 0; i < 2 * NB; ++i)
+                    acc[i >> 1][i & 1] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                        fb[s][p][i & 1], fa[s][p][i >> 1], acc[i >> 1][i & 1], 0, 0, 0);
+        }
+    };
+    const auto multiply = [&](const float *sa, const float *sb) {
+        if (blocks >= 2)
+            multiply_blocks(sa, sb, IC<2>{});
+        else if (blocks == 1)
+            multiply_blocks(sa, sb, IC<1>{});
+    };
+    // Whole slabs first, the next one's loads in flight while one is
+    // multiplied; then what is left, loaded element by element: the last k, or
+    // all of a tile on the edge of an operand whose rows are no multiple of 4.
+    // (In one loop, the choice between the loads made each wait for the last.)
+    const bool fast = (A_KC || m >= kXTile || m % 4 == 0) && (B_KC || n >= kXTile || n % 4 == 0);
+    const int k_whole = fast ? k / kXDeep * kXDeep : 0;
+    f32x4 xa[4], xb[4];
+    int buf = 0;
+    if (k_whole > 0) {
+        load_slab<A_KC>(xa, a, lda, m);
+        load_slab<B_KC>(xb, b, ldb, n);
     }
-    for (int k0 = 0, buf = 0; k0 < k; k0 += kXDeep, buf ^= 1) {
+    for (int k0 = 0; k0 < k_whole; k0 += kXDeep, buf ^= 1) {
         float *sa = lds + buf * 2 * kSlab, *sb = sa + kSlab;
         park_slab<A_KC>(sa, xa);
         park_slab<B_KC>(sb, xb);
         // one barrier per slab: a wave two slabs on would overwrite this
         // buffer, and to get there it has to pass the next barrier
         __syncthreads();
-        if (k0 + kXDeep < k) {
-            a += a_step;
-            b += b_step;
-            load_slab<T, A_KC>(xa, a, lda, m, k - k0 - kXDeep);
-            load_slab<T, B_KC>(xb, b, ldb, n, k - k0 - kXDeep);
+        a += a_step;
+        b += b_step;
+        if (k0 + kXDeep < k_whole) {
+            load_slab<A_KC>(xa, a, lda, m);
+            load_slab<B_KC>(xb, b, ldb, n);
         }
-#pragma unroll
-        for (int kk = 0; kk < kXDeep; kk += 2) {
-            const int row = (kk + half) * kXPitch + l32;
-            float fa[2], fb[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                fa[i] = sa[row + wm + 32 * i];
-                fb[i] = sb[row + wn + 32 * i];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[i >> 1][i & 1] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[i & 1], fa[i >> 1],
-                                                                          acc[i >> 1][i & 1], 0, 0, 0);
-        }
+        multiply(sa, sb);
+    }
+    for (int k0 = k_whole; k0 < k; k0 += kXDeep, buf ^= 1) {
+        float *sa = lds + buf * 2 * kSlab, *sb = sa + kSlab;
+        load_part<A_KC>(xa, a, lda, m, k - k0);
+        load_part<B_KC>(xb, b, ldb, n, k - k0);
+        park_slab<A_KC>(sa, xa);
+        park_slab<B_KC>(sb, xb);
+        __syncthreads();
+        a += a_step;
+        b += b_step;
+        multiply(sa, sb);
     }
 }
 
@@ -163,23 +217,25 @@ __device__ __forceinline__ void store_exact(const f32x16 (&acc)[2][2], uint8_t *
 //           parity c & 1) by the 64 k of iteration c >> 1, in whole 128-byte
 //           lines; fragments are 16-byte reads.  Ring of 5 pieces.
 //   KROWS   m or n contiguous.  Piece c holds the 32 k-rows of half-iteration
-//           c by all 256 columns; fragments are transposing reads.  Ring of 4.
+//           c by all 256 columns; fragments are transposing reads.  Ring of 5
+//           pieces for A, 4 for B.
 // So the product with B as it lies (A LINES, B KROWS), with B transposed
 // (LINES, LINES) and the weight gradient (KROWS, KROWS) are one kernel, none
 // with a transposing pass over memory, in at most 160 KiB of LDS.
 //
 // Why the rings are long enough.  Every phase ends with a wait for the
-// wave's own copies (at most two pieces' in flight; one for B in LINES), for
-// the LDS reads it issued, and a barrier.  Copied by group 0, piece c is issued
-// in phase 2c - 7 and landed by the end of 2c - 3; by group 1, in 2c - 6,
-// landed by the end of 2c - 2 (2c - 4 with one in flight).  First reads:
+// wave's own copies (at most two pieces' in flight; one for B in LINES) and a
+// barrier; the LDS reads of a phase are complete by the end of the next one,
+// whose products need them.  Copied by group 0, piece c is issued in phase
+// 2c - 7 and landed by the end of 2c - 3; by group 1, in 2c - 6, landed by the
+// end of 2c - 2 (2c - 4 with one in flight).  First reads:
 //   A LINES  even pieces by group 0 in phase 2c - 1, odd by group 1 in 2c - 2
 //   A KROWS  2c - 1          B KROWS  2c - 1
 //   B LINES  odd pieces by group 0 in 2c - 3, even in 2c - 1
-// and the piece that c overwrites was last read in
-//   A LINES  2c - 9 (even; c - 5)   or 2c - 10 (odd)
-//   A KROWS  2c - 8 (c - 4)         B KROWS  2c - 8 (c - 4)
-//   B LINES  2c - 8 (c - 5, even)   or 2c - 10 (odd)
+// and the piece that c overwrites was last read, completely, by the end of
+//   A LINES  2c - 8 (c - 5, even) or 2c - 9 (odd)
+//   A KROWS  2c - 9 (c - 5)         B KROWS  2c - 7 (c - 4)
+//   B LINES  2c - 7 (c - 5, even) or 2c - 9 (odd)
 // each before the copy's phase.  Copies past the end of k read nothing
 // (out-of-range offsets) and zero a free piece, so the wait counts are
 // constants.
@@ -187,7 +243,8 @@ enum { LINES = 0, KROWS = 1 };
 
 constexpr int kBig = 256, kPiece = 16384;
 
-constexpr int ring_of(int layout) { return layout == LINES ? 5 : 4; }
+// pieces in the ring of operand A (0) or B (1)
+constexpr int ring_of(int operand, int layout) { return operand == 0 || layout == LINES ? 5 : 4; }
 
 // What one workgroup multiplies: the tile's corner in both operands.
 struct TileWork {
@@ -196,12 +253,13 @@ struct TileWork {
     int m, n, k;           // rows and columns that exist from the corner on; depth
 };
 
-template <int DT, int LA, int LB, int GRP>
+// NB: how many of the group's four 32-row blocks (0, 2 or 4) are multiplied.
+template <int DT, int LA, int LB, int GRP, int NB>
 __device__ __forceinline__ void big_tile_group(f32x16 (&acc)[4][2], const TileWork &w, uint8_t *lds,
                                                int q)
 {
     constexpr int LX = GRP == 0 ? LA : LB;  // layout of the operand this group copies
-    constexpr int RA = ring_of(LA), RB = ring_of(LB);
+    constexpr int RA = ring_of(0, LA);
     constexpr int B_BASE = RA * kPiece;
     const int lane = threadIdx.x & 63;
     const int half = lane >> 5, l32 = lane & 31;
@@ -245,7 +303,7 @@ __device__ __forceinline__ void big_tile_group(f32x16 (&acc)[4][2], const TileWo
         } else {
             const int k0 = c * 32, left = w.k - k0;
             const uint8_t *src = x + (left > 0 ? k0 * ldx : 0) * 2;
-            const uint32_t dst = cp_lds + (uint32_t)(c & 3) * kPiece;
+            const uint32_t dst = cp_lds + (uint32_t)(GRP == 0 ? c % 5 : c & 3) * kPiece;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 copy16(rsrc_words(src), cp_row[j] < left ? off0[j] : kOutOfRange, dst + j * 4096);
@@ -284,15 +342,15 @@ __device__ __forceinline__ void big_tile_group(f32x16 (&acc)[4][2], const TileWo
     u32x4 fa[2][4], fb[2][2];
     auto read_frags = [&](int h) {
         const int even = h & ~1, odd = h & 1;
-        const uint32_t pa = (uint32_t)(LA == LINES ? (even + GRP) % 5 : h & 3) * kPiece;
+        const uint32_t pa = (uint32_t)(LA == LINES ? (even + GRP) % 5 : h % 5) * kPiece;
         const uint32_t pb = B_BASE + (uint32_t)(LB == LINES ? (even + (q >> 1)) % 5 : h & 3) * kPiece;
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < NB; ++i)
                 fa[st][i] = LA == LINES ? read_line(pa, a_line, odd, st, i) : read_tr(pa, a_tr[i], st);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < (NB ? 2 : 0); ++i)
                 fb[st][i] = LB == LINES ? read_line(pb, b_line, odd, st, i) : read_tr(pb, b_tr[i], st);
         }
     };
@@ -300,7 +358,7 @@ __device__ __forceinline__ void big_tile_group(f32x16 (&acc)[4][2], const TileWo
 #pragma unroll
         for (int st = 0; st < 2; ++st)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 2 * NB; ++i)
                 mfma16<DT>(acc[i >> 1][i & 1], fb[st][i & 1], fa[st][i >> 1]);
     };
     // pieces (of four copies) that may be in flight at the end of a phase
@@ -308,13 +366,12 @@ __device__ __forceinline__ void big_tile_group(f32x16 (&acc)[4][2], const TileWo
     auto phase_end = [&]() {
         __builtin_amdgcn_sched_barrier(0);
         wait_vmcnt<kInFlight>();
-        wait_lds();
         barrier_only();
         __builtin_amdgcn_sched_barrier(0);
     };
 
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 2 * NB; ++i)
         acc[i >> 1][i & 1] = f32x16{};
     const int n = (w.k + 31) / 32;
     if (n == 0)
@@ -348,21 +405,36 @@ __device__ __forceinline__ void big_tile_group(f32x16 (&acc)[4][2], const TileWo
     wait_vmcnt<0>();  // the zero-filling copies past the end
 }
 
-// Calls f(accumulators, first row, first column) in every wave once the
-// tile's sums are complete.  Each group has its own copy of everything, so no
-// register value is merged between the groups' paths.
+// Calls f(accumulators, blocks, first row, first column) in every wave once
+// the tile's sums are complete: 32-row blocks 0 .. blocks - 1 (a compile-time
+// constant) hold sums.  A group's last tile is often a low one; its empty
+// blocks are not multiplied (2 or 4 blocks per group, or none), each case in
+// code of its own: branches inside the bursts would have the accumulators
+// spilled.  The wave groups have their own copies of everything too, so no
+// register value is merged between paths.
 template <int DT, int LA, int LB, typename F>
 __device__ __forceinline__ void big_tile(const TileWork &w, uint8_t *lds, F &&f)
 {
-    // wave index as a scalar: the group branch is uniform
+    // wave index as a scalar: the branches are uniform
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     f32x16 acc[4][2];
     if (wave < 4) {
-        big_tile_group<DT, LA, LB, 0>(acc, w, lds, wave);
-        f(acc, 0, wave * 64);
+        if (w.m > 64) {
+            big_tile_group<DT, LA, LB, 0, 4>(acc, w, lds, wave);
+            f(acc, IC<4>{}, 0, wave * 64);
+        } else {
+            big_tile_group<DT, LA, LB, 0, 2>(acc, w, lds, wave);
+            f(acc, IC<2>{}, 0, wave * 64);
+        }
+    } else if (w.m > 192) {
+        big_tile_group<DT, LA, LB, 1, 4>(acc, w, lds, wave - 4);
+        f(acc, IC<4>{}, 128, (wave - 4) * 64);
+    } else if (w.m > 128) {
+        big_tile_group<DT, LA, LB, 1, 2>(acc, w, lds, wave - 4);
+        f(acc, IC<2>{}, 128, (wave - 4) * 64);
     } else {
-        big_tile_group<DT, LA, LB, 1>(acc, w, lds, wave - 4);
-        f(acc, 128, (wave - 4) * 64);
+        big_tile_group<DT, LA, LB, 1, 0>(acc, w, lds, wave - 4);
+        f(acc, IC<0>{}, 128, (wave - 4) * 64);
     }
 }
 
