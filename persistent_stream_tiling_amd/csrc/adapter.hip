@@ -538,7 +538,7 @@ template <int DT, int LB>
 __global__ __launch_bounds__(512, 1) void adapter_big_kernel(AdapterArgs a)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[(ring_of(0, LINES) + ring_of(1, LB)) * kPiece];
-    static_assert(adapters_lds<DT, kBig, 2>() <= sizeof(lds), "LDS");
+    static_assert(adapters_lds<DT, kBig, 2>() <= 5 * kPiece && 5 * kPiece + 8 * 4096 <= sizeof(lds), "LDS");
     int tm, tn;
     if (!find_tile(a, (int)blockIdx.x, &tm, &tn))
         return;
@@ -546,15 +546,18 @@ __global__ __launch_bounds__(512, 1) void adapter_big_kernel(AdapterArgs a)
     const TileWork w = shared_work<LB>(a, m0, n0, 0, a.K);
     const __amdgpu_buffer_rsrc_t c = c_rows(a, m0);
     const bool vec = a.c_vec || n0 + kBig <= a.N;
+    const bool whole = n0 + kBig <= a.N || a.N % (a.c_dtype ? 8 : 4) == 0;
     big_tile<DT, LINES, LB>(w, lds, [&](f32x16 (&acc)[4][2], auto blocks, int row, int col) {
         constexpr int kBlocks = decltype(blocks)::value;
         // (a group without rows takes part in the splitting of H)
         add_adapters<DT, kBig, kBlocks, 2>(
             reinterpret_cast<f32x16(&)[kBlocks ? kBlocks : 1][2]>(acc), a, lds, m0, row, n0 + col, 0, 1);
+        // (past the terms, which other waves may still read)
+        uint8_t *const mine = lds + 5 * kPiece + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * 4096;
 #pragma unroll
-        for (int i = 0; i < 2 * kBlocks; ++i)
-            store_block(acc[i >> 1][i & 1], c, c_row_bytes(a), row + (i >> 1) * 32, w.m,
-                        n0 + col + (i & 1) * 32, a.N, vec, a.c_dtype);
+        for (int i = 0; i < kBlocks; ++i)
+            store_lines(acc[i][0], acc[i][1], mine, c, c_row_bytes(a), row + 32 * i, w.m, n0 + col, a.N,
+                        whole, vec, a.c_dtype);
     });
 }
 

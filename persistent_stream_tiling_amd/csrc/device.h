@@ -88,7 +88,8 @@ __device__ __forceinline__ void store_block(const f32x16 &blk, __amdgpu_buffer_r
                                             uint32_t row_bytes, int brow, int rows_ok, int col,
                                             int N, bool vec, int c_dtype)
 {
-    const int lane = threadIdx.x & 63;
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // (as in store_lines)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const f32x4 q0 = f32x4{blk[8 * j], blk[8 * j + 1], blk[8 * j + 2], blk[8 * j + 3]};
@@ -111,6 +112,70 @@ __device__ __forceinline__ void store_block(const f32x16 &blk, __amdgpu_buffer_r
             const int row = brow + (lane & 31), n = col + 16 * j + 4 * (lane >> 5);
             store_four(q0, c, (uint32_t)row * row_bytes, n, N, row < rows_ok, false, c_dtype);
             store_four(q1, c, (uint32_t)row * row_bytes, n + 8, N, row < rows_ok, false, c_dtype);
+        }
+    }
+}
+
+// A wave's 32 rows by 64 columns (two accumulator blocks side by side) to C, in
+// whole 128-byte lines: the caches take a store line by line, and from the
+// accumulators' order a store would touch 16 lines for 512 or 1024 bytes (a
+// 256x256 bf16 tile took 9 us to store, all CUs at it).  So 32 rows of 128
+// bytes (64 columns of 16 bits, or 32 of 32) pass through 4 KiB of LDS of the
+// wave's own: 16-byte chunk c of row r sits at c ^ (r & 7), which keeps writes
+// and reads free of bank conflicts, and each store covers 8 rows.  Where a
+// chunk could straddle C's last column (`whole` false) blocks are stored as
+// they lie.
+__device__ __forceinline__ void store_lines(const f32x16 &left, const f32x16 &right, uint8_t *lds,
+                                            __amdgpu_buffer_rsrc_t c, uint32_t row_bytes, int brow,
+                                            int rows_ok, int col, int N, bool whole, bool vec,
+                                            int c_dtype)
+{
+    if (!whole) {
+        store_block(left, c, row_bytes, brow, rows_ok, col, N, vec, c_dtype);
+        store_block(right, c, row_bytes, brow, rows_ok, col + 32, N, vec, c_dtype);
+        return;
+    }
+    // (opaque, so that the addresses below are formed here: formed once, ahead of
+    // a loop over tiles, they would occupy registers its products need)
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int row = lane & 31, half = lane >> 5;
+    const auto at = [](int r, int chunk) { return (uint32_t)(r * 128 + ((chunk ^ (r & 7)) << 4)); };
+    // the rows' 128 bytes from column n on
+    const auto send = [&](int n, int columns_per_chunk) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 3), chunk = (lane & 7) ^ (r & 7);
+            const u32x4 v = *(const u32x4 *)(lds + r * 128 + ((lane & 7) << 4));
+            const int cn = n + chunk * columns_per_chunk;
+            const uint32_t off = (uint32_t)(brow + r) * row_bytes + (uint32_t)cn * (16 / columns_per_chunk);
+            __builtin_amdgcn_raw_buffer_store_b128(
+                v, c, (int)(brow + r < rows_ok && cn < N ? off : kOutOfRange), 0, 0);
+        }
+    };
+    if (c_dtype != 0) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f32x16 &b = j ? right : left;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    h[e] = c_dtype == 1 ? f16_bits(b[4 * g + e]) : bf16_bits(b[4 * g + e]);
+                *(u32x2 *)(lds + at(row, 4 * j + g) + 8 * half) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+            }
+        }
+        send(col, 8);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f32x16 &b = j ? right : left;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *(u32x4 *)(lds + at(row, 2 * g + half)) = u32x4{bits_of(b[4 * g]), bits_of(b[4 * g + 1]),
+                                                              bits_of(b[4 * g + 2]), bits_of(b[4 * g + 3])};
+            send(col + 32 * j, 4);
         }
     }
 }

@@ -29,6 +29,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t c_rows(const GroupedArgs &a, i
     return make_rsrc(a.C + row * c_row_bytes(a));
 }
 
+constexpr int kMaxGroups = 4096;
+
 template <bool B_KC>
 __global__ __launch_bounds__(kXThreads, 2) void rows_exact_kernel(GroupedArgs a)
 {
@@ -78,25 +80,6 @@ __device__ __forceinline__ TileWork rows_work(const GroupedArgs &a, const RowTil
     return w;
 }
 
-template <int DT, int LB>
-__global__ __launch_bounds__(512, 1) void rows_big_kernel(GroupedArgs a)
-{
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[(ring_of(0, LINES) + ring_of(1, LB)) * kPiece];
-    RowTile t;
-    if (!find_row_tile<kBig>(a, blockIdx.x, &t))
-        return;
-    const int n0 = t.tn * kBig;
-    const TileWork w = rows_work<LB>(a, t, n0);
-    const __amdgpu_buffer_rsrc_t c = c_rows(a, t.m0);
-    const bool vec = a.c_vec || n0 + kBig <= a.N;
-    big_tile<DT, LINES, LB>(w, lds, [&](const f32x16 (&acc)[4][2], auto blocks, int row, int col) {
-#pragma unroll
-        for (int i = 0; i < 2 * decltype(blocks)::value; ++i)
-            store_block(acc[i >> 1][i & 1], c, c_row_bytes(a), row + (i >> 1) * 32, w.m,
-                        n0 + col + (i & 1) * 32, a.N, vec, a.c_dtype);
-    });
-}
-
 template <int DT, int LB, int MT>
 __global__ __launch_bounds__(256, 2) void rows_narrow_kernel(GroupedArgs a)
 {
@@ -116,40 +99,191 @@ __global__ __launch_bounds__(256, 2) void rows_narrow_kernel(GroupedArgs a)
         store_block(acc[i][0], c, c_row_bytes(a), i * 32, w.m, n0 + wave * 32, a.N, vec, a.c_dtype);
 }
 
+// ---- 256x256 tiles: a launch of one workgroup lists the tiles, then a workgroup
+// per CU takes them from queues.
+
+struct TileList {
+    TileQueues queues;
+    // rows products: one entry per row tile; weight gradient: one per group
+    struct Entry {
+        int32_t g, lo, hi, pad;  // group; rows [lo, hi) of the tile's group from the tile on
+    } entry[1];
+};
+
+constexpr int kPlanThreads = 1024;
+
+// Lists the row tiles of all groups (the rows past the last one too), in order;
+// each die's queue is a run of row tiles, so a group's matrix is read into one
+// die's L2, or two.  (Low tiles last, to even out the queues' ends, measured no
+// better: 451 against 444 us for the experts' batch.)  `most` entries fit the
+// list: enough for ascending offsets.
+__global__ __launch_bounds__(kPlanThreads) void plan_rows_kernel(GroupedArgs a, TileList *list,
+                                                                 int32_t most, int32_t workgroups)
+{
+    __shared__ int32_t starts[kMaxGroups + 2];  // a group's first row tile
+    __shared__ int64_t wave_sum[kPlanThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int32_t runs = a.groups + 1, each = (runs + kPlanThreads - 1) / kPlanThreads;
+    const int32_t g_lo = tid * each < runs ? tid * each : runs;
+    const int32_t g_hi = g_lo + each < runs ? g_lo + each : runs;
+    const auto tiles_of = [&](int32_t g) {
+        int32_t lo, hi;
+        group_rows(a.offsets, g, a.groups, a.rows, &lo, &hi);
+        return ((int64_t)hi - lo + kBig - 1) / kBig;
+    };
+    int64_t mine = 0;
+    for (int32_t g = g_lo; g < g_hi; ++g)
+        mine += tiles_of(g);
+    int64_t sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t up = __shfl_up(sum, d);
+        sum += lane >= d ? up : 0;
+    }
+    if (lane == 63)
+        wave_sum[wave] = sum;
+    __syncthreads();
+    int64_t at = sum - mine;
+    for (int w = 0; w < wave; ++w)
+        at += wave_sum[w];
+    for (int32_t g = g_lo; g < g_hi; ++g) {
+        starts[g] = (int32_t)(at < most ? at : most);
+        at += tiles_of(g);
+        if (g == a.groups)
+            starts[runs] = (int32_t)(at < most ? at : most);
+    }
+    __syncthreads();
+    const int32_t total = starts[runs];
+    for (int32_t t = tid; t < total; t += kPlanThreads) {
+        // the last group that starts at or before t (an empty one starts where
+        // the next does)
+        int32_t from = 0, to = runs;
+        while (to - from > 1) {
+            const int32_t mid = (from + to) >> 1;
+            if (starts[mid] <= t)
+                from = mid;
+            else
+                to = mid;
+        }
+        int32_t lo, hi;
+        group_rows(a.offsets, from, a.groups, a.rows, &lo, &hi);
+        list->entry[t] = TileList::Entry{from, lo + (t - starts[from]) * kBig, hi, 0};
+    }
+    if (tid < kQueues) {
+        const int32_t share = (total + kQueues - 1) / kQueues;
+        const int32_t begin = tid * share < total ? tid * share : total;
+        const int32_t end = begin + share < total ? begin + share : total;
+        fill_queue(&list->queues, tid, begin * a.tiles_n, end * a.tiles_n, workgroups);
+    }
+}
+
+// Lists the groups by size, largest first (a tile's time is its group's rows),
+// dealt to the dies' queues to and fro.  Above kSortGroups groups they keep
+// their order: comparing all pairs would take longer than it saves.
+constexpr int kSortGroups = 1024;
+
+__global__ __launch_bounds__(kPlanThreads) void plan_groups_kernel(GroupedArgs a, TileList *list,
+                                                                   int32_t workgroups)
+{
+    __shared__ int32_t size[kSortGroups];
+    const int tid = threadIdx.x;
+    const bool sorts = a.groups <= kSortGroups;
+    if (sorts && tid < a.groups) {
+        int32_t lo, hi;
+        group_rows(a.offsets, tid, a.groups, a.rows, &lo, &hi);
+        size[tid] = hi - lo;
+    }
+    __syncthreads();
+    const auto base = [&](int x) {  // entries of the queues before x
+        const int whole = a.groups / kQueues, rest = a.groups % kQueues;
+        int n = 0;
+        for (int i = 0; i < x; ++i)
+            n += whole + ((whole & 1 ? kQueues - 1 - i : i) < rest ? 1 : 0);
+        return n;
+    };
+    for (int32_t g = tid; g < a.groups; g += kPlanThreads) {
+        int32_t rank = g;
+        if (sorts) {
+            rank = 0;
+            for (int32_t o = 0; o < a.groups; ++o)
+                rank += size[o] > size[g] || (size[o] == size[g] && o < g) ? 1 : 0;
+        }
+        const int row = rank / kQueues, col = rank % kQueues;
+        int32_t lo, hi;
+        group_rows(a.offsets, g, a.groups, a.rows, &lo, &hi);
+        list->entry[base(row & 1 ? kQueues - 1 - col : col) + row] = TileList::Entry{g, lo, hi, 0};
+    }
+    if (tid < kQueues) {
+        const int32_t per = a.tiles_m * a.tiles_n;
+        fill_queue(&list->queues, tid, base(tid) * per, base(tid + 1) * per, workgroups);
+    }
+}
+
+// (lds: 4 KiB of the wave's own)
+__device__ __forceinline__ void store_big(const GroupedArgs &a, const f32x16 (&acc)[4][2], int blocks,
+                                          const TilePlace &p, uint8_t *lds, int row, int col)
+{
+    const __amdgpu_buffer_rsrc_t c = make_rsrc(p.c);
+    const bool inside = p.n0 + kBig <= a.N;
+    const bool whole = inside || a.N % (a.c_dtype ? 8 : 4) == 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < blocks) {
+            store_lines(acc[i][0], acc[i][1], lds, c, c_row_bytes(a), row + i * 32, p.m, p.n0 + col, a.N,
+                        whole, a.c_vec || inside, a.c_dtype);
+            __builtin_amdgcn_sched_barrier(0);  // (one block's registers at a time)
+        }
+}
+
+template <int DT, int LB>
+__global__ __launch_bounds__(512, 1) void rows_big_kernel(GroupedArgs a, TileList *list)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[(ring_of(0, LINES) + ring_of(1, LB)) * kPiece];
+    big_tiles<DT, LINES, LB>(
+        &list->queues, lds,
+        [&](int id, TileWork *w, TilePlace *p) {
+            const TileList::Entry e = list->entry[id / a.tiles_n];
+            const RowTile t{e.g, e.lo, e.hi, id % a.tiles_n};
+            p->n0 = t.tn * kBig;
+            p->m = e.hi - e.lo;
+            p->c = a.C + (int64_t)e.lo * c_row_bytes(a);
+            *w = rows_work<LB>(a, t, p->n0);
+        },
+        [&](const f32x16 (&acc)[4][2], auto blocks, const TilePlace &p, int row, int col) {
+            store_big(a, acc, decltype(blocks)::value, p, store_lds(lds), row, col);
+        });
+}
+
 template <int DT>
-__global__ __launch_bounds__(512, 1) void wgrad_big_kernel(GroupedArgs a)
+__global__ __launch_bounds__(512, 1) void wgrad_big_kernel(GroupedArgs a, TileList *list)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[(ring_of(0, KROWS) + ring_of(1, KROWS)) * kPiece];
-    const int64_t per = (int64_t)a.tiles_m * a.tiles_n;
-    const int32_t g = (int32_t)(blockIdx.x / per);
-    const int32_t in = (int32_t)(blockIdx.x - g * per);
-    const int m0 = in / a.tiles_n * kBig, n0 = in % a.tiles_n * kBig;
-    int32_t lo, hi;
-    group_rows(a.offsets, g, a.groups, a.rows, &lo, &hi);
-    TileWork w;
-    w.a = a.A + ((int64_t)lo * a.lda + m0) * 2;
-    w.b = a.B + ((int64_t)lo * a.ldb + n0) * 2;
-    w.lda = a.lda;
-    w.ldb = a.ldb;
-    w.m = a.M - m0;
-    w.n = a.N - n0;
-    w.k = hi - lo;
-    const __amdgpu_buffer_rsrc_t c = c_rows(a, (int64_t)g * a.M + m0);
-    const bool vec = a.c_vec || n0 + kBig <= a.N;
-    big_tile<DT, KROWS, KROWS>(w, lds, [&](const f32x16 (&acc)[4][2], auto blocks, int row, int col) {
-#pragma unroll
-        for (int i = 0; i < 2 * decltype(blocks)::value; ++i)
-            store_block(acc[i >> 1][i & 1], c, c_row_bytes(a), row + (i >> 1) * 32, w.m,
-                        n0 + col + (i & 1) * 32, a.N, vec, a.c_dtype);
-    });
+    big_tiles<DT, KROWS, KROWS>(
+        &list->queues, lds,
+        [&](int id, TileWork *w, TilePlace *p) {
+            const int per = a.tiles_m * a.tiles_n, in = id % per;
+            const TileList::Entry e = list->entry[id / per];
+            const int m0 = in / a.tiles_n * kBig;
+            p->n0 = in % a.tiles_n * kBig;
+            p->m = a.M - m0;
+            p->c = a.C + ((int64_t)e.g * a.M + m0) * c_row_bytes(a);
+            w->a = a.A + ((int64_t)e.lo * a.lda + m0) * 2;
+            w->b = a.B + ((int64_t)e.lo * a.ldb + p->n0) * 2;
+            w->lda = a.lda;
+            w->ldb = a.ldb;
+            w->m = p->m;
+            w->n = a.N - p->n0;
+            w->k = e.hi - e.lo;
+        },
+        [&](const f32x16 (&acc)[4][2], auto blocks, const TilePlace &p, int row, int col) {
+            store_big(a, acc, decltype(blocks)::value, p, store_lds(lds), row, col);
+        });
 }
 
 int elem_bytes(int dtype)
 {
     return dtype == GEMM_F32 ? 4 : (dtype == GEMM_F16 || dtype == GEMM_BF16 ? 2 : 0);
 }
-
-constexpr int kMaxGroups = 4096;
 
 // Shared argument checks of both products; 0 or -1.
 int check(const gemm_grouped *p)
@@ -195,7 +329,9 @@ int check(const gemm_grouped *p)
 struct Layout {
     int64_t lda, ldb, b_rows, b_cols;
     bool pack_a, pack_b;
-    size_t off_b, bytes;
+    int mt;                  // row blocks of the few-rows tiles, 0: 256x256
+    int64_t tiles_m, tiles_n;// weight gradient: of C; rows products: row tiles at most
+    size_t off_b, off_list, bytes;
 };
 
 // Row blocks of 32 per tile of the few-rows kernel, 0 for 256x256 tiles, by
@@ -215,6 +351,8 @@ int narrow_mt(const gemm_grouped *p)
     return mean <= 8 ? 1 : (mean <= 48 ? 2 : 4);
 }
 
+constexpr int kCus = 256;  // workgroups that take tiles from the queues
+
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
 Layout layout(const gemm_grouped *p)
@@ -229,7 +367,20 @@ Layout layout(const gemm_grouped *p)
     l.lda = l.pack_a ? (p->K + 7) / 8 * 8 : p->K;
     l.ldb = l.pack_b ? (l.b_cols + 7) / 8 * 8 : l.b_cols;
     l.off_b = l.pack_a ? align_up((size_t)p->rows * l.lda * E) : 0;
-    l.bytes = l.off_b + (l.pack_b ? align_up((size_t)l.b_rows * l.ldb * E) : 0);
+    l.off_list = l.off_b + (l.pack_b ? align_up((size_t)l.b_rows * l.ldb * E) : 0);
+    const bool wgrad = p->op == GEMM_GROUPED_WGRAD;
+    l.mt = E == 4 || wgrad ? 0 : narrow_mt(p);
+    const int bm = E == 4 ? kXTile : (l.mt ? 32 * l.mt : kBig);
+    const int bn = E == 4 ? kXTile : (l.mt ? kNarrow : kBig);
+    l.tiles_n = (p->N + bn - 1) / bn;
+    // a group's rows, and those past the last group, end inside a tile
+    const int64_t ends = p->groups + 1 < p->rows ? p->groups + 1 : p->rows;
+    l.tiles_m = wgrad ? (p->K + bm - 1) / bm : p->rows / bm + ends;
+    const bool listed = E == 2 && !l.mt;
+    l.bytes = l.off_list;
+    if (listed)
+        l.bytes += align_up(sizeof(TileList) +
+                            (size_t)(wgrad ? p->groups : l.tiles_m) * sizeof(TileList::Entry));
     return l;
 }
 
@@ -284,21 +435,12 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
     a.c_dtype = c_dtype;
     a.c_vec = p->N % 4 == 0 && ((uintptr_t)C & (4 * CE - 1)) == 0;
     a.xcds = 8;
-    const int mt = E == 4 || wgrad ? 0 : narrow_mt(p);
-    const int bm = E == 4 ? kXTile : (mt ? 32 * mt : kBig);
-    const int bn = E == 4 ? kXTile : (mt ? kNarrow : kBig);
-    const int threads = E == 4 || mt ? 256 : 512;
-    a.tiles_n = (int32_t)((p->N + bn - 1) / bn);
-    a.tiles_m = (int32_t)((p->K + bm - 1) / bm);
-    int64_t tiles;
-    if (wgrad) {
-        tiles = (int64_t)p->groups * a.tiles_m * a.tiles_n;
-    } else {
-        // a group's rows, and those past the last group, end inside a tile
-        const int64_t ends = p->groups + 1 < p->rows ? p->groups + 1 : p->rows;
-        tiles = (p->rows / bm + ends) * a.tiles_n;
+    const int mt = l.mt, threads = E == 4 || mt ? 256 : 512;
+    a.tiles_n = (int32_t)l.tiles_n;
+    a.tiles_m = (int32_t)l.tiles_m;
+    int64_t tiles = l.tiles_m * l.tiles_n * (wgrad ? p->groups : 1);
+    if (!wgrad)
         tiles = (tiles + a.xcds - 1) / a.xcds * a.xcds;
-    }
     if (tiles >= ((int64_t)1 << 32) / threads) {
         set_error("too many tiles for one launch (%lld)", (long long)tiles);
         return -1;
@@ -320,12 +462,21 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
         if (l.pack_b)
             a.B = ws + l.off_b;
     }
+    const int32_t stay = tiles < kCus ? (int32_t)tiles : kCus;  // workgroups that take tiles
+    TileList *const list = (TileList *)((uint8_t *)workspace + l.off_list);
+#define GSK_BIG(KERNEL, ...)                                                                     \
+    hipLaunchKernelGGL((KERNEL<__VA_ARGS__>), dim3((unsigned)stay), dim3(threads), 0, s, a, list)
+    if (E == 2 && wgrad)
+        hipLaunchKernelGGL(plan_groups_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, list, stay);
+    else if (E == 2 && !mt)
+        hipLaunchKernelGGL(plan_rows_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, list, a.tiles_m,
+                           stay);
 #define GSK_GROUPED(KERNEL, ...)                                                                 \
     hipLaunchKernelGGL((KERNEL<__VA_ARGS__>), dim3((unsigned)tiles), dim3(threads), 0, s, a)
 #define GSK_GROUPED_16(DT)                                                                       \
     do {                                                                                         \
         if (wgrad)                                                                               \
-            GSK_GROUPED(wgrad_big_kernel, DT);                                                   \
+            GSK_BIG(wgrad_big_kernel, DT);                                                       \
         else if (mt == 1 && bt)                                                                  \
             GSK_GROUPED(rows_narrow_kernel, DT, LINES, 1);                                       \
         else if (mt == 1)                                                                        \
@@ -339,9 +490,9 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
         else if (mt == 4)                                                                        \
             GSK_GROUPED(rows_narrow_kernel, DT, KROWS, 4);                                       \
         else if (bt)                                                                             \
-            GSK_GROUPED(rows_big_kernel, DT, LINES);                                             \
+            GSK_BIG(rows_big_kernel, DT, LINES);                                                 \
         else                                                                                     \
-            GSK_GROUPED(rows_big_kernel, DT, KROWS);                                             \
+            GSK_BIG(rows_big_kernel, DT, KROWS);                                                 \
     } while (0)
     if (E == 4) {
         if (wgrad)
@@ -357,6 +508,7 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
     }
 #undef GSK_GROUPED_16
 #undef GSK_GROUPED
+#undef GSK_BIG
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) {
         set_error("grouped product launch failed: %s", hipGetErrorString(e));

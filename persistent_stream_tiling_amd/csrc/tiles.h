@@ -253,189 +253,380 @@ struct TileWork {
     int m, n, k;           // rows and columns that exist from the corner on; depth
 };
 
-// NB: how many of the group's four 32-row blocks (0, 2 or 4) are multiplied.
-template <int DT, int LA, int LB, int GRP, int NB>
-__device__ __forceinline__ void big_tile_group(f32x16 (&acc)[4][2], const TileWork &w, uint8_t *lds,
-                                               int q)
-{
-    constexpr int LX = GRP == 0 ? LA : LB;  // layout of the operand this group copies
-    constexpr int RA = ring_of(0, LA);
-    constexpr int B_BASE = RA * kPiece;
-    const int lane = threadIdx.x & 63;
-    const int half = lane >> 5, l32 = lane & 31;
-    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(lds));
+// One wave group's side of the tile: where it copies from and reads.
+template <int DT, int LA, int LB, int GRP>
+struct BigGroup {
+    static constexpr int LX = GRP == 0 ? LA : LB;  // layout of the operand this group copies
+    static constexpr int B_BASE = ring_of(0, LA) * kPiece;
+    // pieces (of four copies) that may be in flight at the end of a phase
+    static constexpr int kInFlight = (GRP == 1 && LB == LINES ? 1 : 2) * 4;
 
-    // Copies: copy j of this wave fills KiB 4j + q of a piece.
-    const uint8_t *x = GRP == 0 ? w.a : w.b;
-    const int64_t ldx = GRP == 0 ? w.lda : w.ldb;
-    const int have = GRP == 0 ? w.m : w.n;  // rows (LINES) or columns (KROWS) that exist
-    int cp_row[4], cp_chunk[4];
+    uint8_t *lds;
+    int q;
+    // copies: copy j of this wave fills KiB 4j + q of a piece
+    const uint8_t *x;
+    int64_t ldx;
+    int k;
+    uint32_t cp_lds;
     uint32_t off0[4], off1[4];  // LINES: even and odd pieces
+    // fragment reads
+    uint32_t a_line, b_line, a_tr[4], b_tr[2];
+
+    static __device__ __forceinline__ int cp_row(int j, int q)
+    {
+        const int lane = threadIdx.x & 63;
+        return LX == LINES ? 8 * (4 * j + q) + (lane >> 3) : 2 * (4 * j + q) + (lane >> 5);
+    }
+    static __device__ __forceinline__ int cp_chunk(int j, int q)
+    {
+        const int lane = threadIdx.x & 63, row = cp_row(j, q);
+        return LX == LINES ? (lane & 7) ^ (int)swz_row(row) : (lane & 31) ^ (int)swz_krow(row);
+    }
+
+    __device__ __forceinline__ BigGroup(uint8_t *lds_, int q_) : lds(lds_), q(q_)
+    {
+        // Fragment reads: lane l gets row (or column) l % 32 of a 32-wide block
+        // at k 8 * (l / 32) .. + 7 of a 16-deep step, two steps per
+        // half-iteration.
+        const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+        const int g4 = lane >> 4, si = lane & 15, krow = 8 * (g4 >> 1) + (si >> 2);
+        const auto line = [&](int r0) { return (uint32_t)(r0 * 128) + ((half ^ swz_row(r0)) << 4); };
+        const auto krows = [&](int col) {
+            const int n = col + 16 * (g4 & 1) + 4 * (si & 3);
+            return (uint32_t)(krow * 512 + (((n >> 3) ^ (int)swz_krow(krow)) << 4) + (n & 7) * 2);
+        };
+        a_line = line(l32);
+        b_line = line((q & 1) * 64 + l32);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if constexpr (LX == LINES) {
-            cp_row[j] = 8 * (4 * j + q) + (lane >> 3);
-            cp_chunk[j] = (lane & 7) ^ (int)swz_row(cp_row[j]);
-            const uint32_t o = (uint32_t)(cp_row[j] * (int)ldx * 2 + (cp_chunk[j] << 4));
-            off0[j] = cp_row[j] < have ? o : kOutOfRange;
-            off1[j] = cp_row[j] + 128 < have ? o + (uint32_t)(256 * (int)ldx) : kOutOfRange;
-        } else {
-            cp_row[j] = 2 * (4 * j + q) + (lane >> 5);
-            cp_chunk[j] = (lane & 31) ^ (int)swz_krow(cp_row[j]);
-            off0[j] = cp_chunk[j] * 8 < have
-                          ? (uint32_t)(cp_row[j] * (int)ldx * 2 + (cp_chunk[j] << 4))
-                          : kOutOfRange;
-            off1[j] = off0[j];
+        for (int i = 0; i < 4; ++i)
+            a_tr[i] = krows(GRP * 128 + i * 32);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            b_tr[i] = krows(q * 64 + i * 32);
+        cp_lds = __builtin_amdgcn_readfirstlane(lds_address(lds)) + (uint32_t)(GRP == 0 ? 0 : B_BASE) +
+                 (uint32_t)q * 1024;
+    }
+
+    __device__ __forceinline__ void set(const TileWork &w)
+    {
+        x = GRP == 0 ? w.a : w.b;
+        ldx = GRP == 0 ? w.lda : w.ldb;
+        k = w.k;
+        const int have = GRP == 0 ? w.m : w.n;  // rows (LINES) or columns (KROWS) that exist
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = cp_row(j, q), chunk = cp_chunk(j, q);
+            const uint32_t o = (uint32_t)(row * (int)ldx * 2 + (chunk << 4));
+            if constexpr (LX == LINES) {
+                off0[j] = row < have ? o : kOutOfRange;
+                off1[j] = row + 128 < have ? o + (uint32_t)(256 * (int)ldx) : kOutOfRange;
+            } else {
+                off0[j] = chunk * 8 < have ? o : kOutOfRange;
+            }
         }
     }
-    const uint32_t cp_lds = lds0 + (uint32_t)(GRP == 0 ? 0 : B_BASE) + (uint32_t)q * 1024;
-    auto copy_piece = [&](int c) {
+
+    __device__ __forceinline__ void copy_piece(int c) const
+    {
         if constexpr (LX == LINES) {
-            const int k0 = (c >> 1) * 64, left = w.k - k0;
+            const int k0 = (c >> 1) * 64, left = k - k0;
             const uint8_t *src = x + (left > 0 ? k0 : 0) * 2;
             const uint32_t dst = cp_lds + (uint32_t)(c % 5) * kPiece;
             const bool odd = c & 1;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t off = odd ? off1[j] : off0[j];
-                copy16(rsrc_words(src), cp_chunk[j] * 8 < left ? off : kOutOfRange, dst + j * 4096);
+                copy16(rsrc_words(src), cp_chunk(j, q) * 8 < left ? off : kOutOfRange, dst + j * 4096);
             }
         } else {
-            const int k0 = c * 32, left = w.k - k0;
+            const int k0 = c * 32, left = k - k0;
             const uint8_t *src = x + (left > 0 ? k0 * ldx : 0) * 2;
             const uint32_t dst = cp_lds + (uint32_t)(GRP == 0 ? c % 5 : c & 3) * kPiece;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                copy16(rsrc_words(src), cp_row[j] < left ? off0[j] : kOutOfRange, dst + j * 4096);
+                copy16(rsrc_words(src), cp_row(j, q) < left ? off0[j] : kOutOfRange, dst + j * 4096);
         }
-    };
+    }
 
-    // Fragment reads: lane l gets row (or column) l % 32 of a 32-wide block at
-    // k 8 * (l / 32) .. + 7 of a 16-deep step, two steps per half-iteration.
-    const int g4 = lane >> 4, si = lane & 15;
-    const int tr_krow = 8 * (g4 >> 1) + (si >> 2);
-    auto lines_lane = [&](int r0) { return (uint32_t)(r0 * 128) + ((half ^ swz_row(r0)) << 4); };
-    auto krows_lane = [&](int col) {
-        const int n = col + 16 * (g4 & 1) + 4 * (si & 3);
-        return (uint32_t)(tr_krow * 512 + (((n >> 3) ^ (int)swz_krow(tr_krow)) << 4) + (n & 7) * 2);
-    };
-    const uint32_t a_line = lines_lane(l32), b_line = lines_lane((q & 1) * 64 + l32);
-    uint32_t a_tr[4], b_tr[2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        a_tr[i] = krows_lane(GRP * 128 + i * 32);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        b_tr[i] = krows_lane(q * 64 + i * 32);
+    // The first copies of a tile, issued before run().
+    __device__ __forceinline__ void start() const
+    {
+        copy_piece(0);
+        copy_piece(1);
+        copy_piece(2);
+    }
+
+    static __device__ __forceinline__ void phase_end()
+    {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<kInFlight>();
+        barrier_only();
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
     // block i (32 rows on: bit 2 of the swizzle flips) of a LINES piece
-    auto read_line = [&](uint32_t piece, uint32_t line, int odd, int st, int i) {
-        const uint32_t xor_bits = (uint32_t)(st << 5) | (uint32_t)((i & 1) << 6);
-        return *(const u32x4 *)(lds + piece + i * 4096 + ((line ^ ((uint32_t)odd << 6)) ^ xor_bits));
-    };
-    auto read_tr = [&](uint32_t piece, uint32_t tr, int st) {
+    __device__ __forceinline__ u32x4 read_line(uint32_t piece, uint32_t line, int odd, int st, int i) const
+    {
+        const uint32_t bits = (uint32_t)(st << 5) | (uint32_t)((i & 1) << 6);
+        return *(const u32x4 *)(lds + piece + i * 4096 + ((line ^ ((uint32_t)odd << 6)) ^ bits));
+    }
+    __device__ __forceinline__ u32x4 read_tr(uint32_t piece, uint32_t tr, int st) const
+    {
         const uint8_t *p = lds + piece + tr + st * 16 * 512;
         const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(GSK_LDS_PTR(i16x4, p));
         const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(GSK_LDS_PTR(i16x4, p + 4 * 512));
         const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
         return u32x4{l2[0], l2[1], h2[0], h2[1]};
-    };
-    u32x4 fa[2][4], fb[2][2];
-    auto read_frags = [&](int h) {
-        const int even = h & ~1, odd = h & 1;
-        const uint32_t pa = (uint32_t)(LA == LINES ? (even + GRP) % 5 : h % 5) * kPiece;
-        const uint32_t pb = B_BASE + (uint32_t)(LB == LINES ? (even + (q >> 1)) % 5 : h & 3) * kPiece;
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-                fa[st][i] = LA == LINES ? read_line(pa, a_line, odd, st, i) : read_tr(pa, a_tr[i], st);
-#pragma unroll
-            for (int i = 0; i < (NB ? 2 : 0); ++i)
-                fb[st][i] = LB == LINES ? read_line(pb, b_line, odd, st, i) : read_tr(pb, b_tr[i], st);
-        }
-    };
-    auto multiply = [&]() {
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-            for (int i = 0; i < 2 * NB; ++i)
-                mfma16<DT>(acc[i >> 1][i & 1], fb[st][i & 1], fa[st][i >> 1]);
-    };
-    // pieces (of four copies) that may be in flight at the end of a phase
-    constexpr int kInFlight = (GRP == 1 && LB == LINES ? 1 : 2) * 4;
-    auto phase_end = [&]() {
-        __builtin_amdgcn_sched_barrier(0);
-        wait_vmcnt<kInFlight>();
-        barrier_only();
-        __builtin_amdgcn_sched_barrier(0);
-    };
-
-#pragma unroll
-    for (int i = 0; i < 2 * NB; ++i)
-        acc[i >> 1][i & 1] = f32x16{};
-    const int n = (w.k + 31) / 32;
-    if (n == 0)
-        return;
-    copy_piece(0);
-    copy_piece(1);
-    copy_piece(2);
-    phase_end();
-    if constexpr (GRP == 0) {
-        copy_piece(3);
-        read_frags(0);
     }
-    phase_end();
-    for (int h = 0; h < n; ++h) {
-        if constexpr (GRP == 0) {
-            multiply();
+
+    // acc = the sums of the tile that set() described and start() began, of the
+    // group's first NB 32-row blocks (0, 2 or 4): a group of rows often ends in
+    // a low tile, whose empty blocks are not multiplied.  NB is a template case
+    // because branches inside the bursts had the accumulators spilled.
+    template <int NB>
+    __device__ __forceinline__ void run(f32x16 (&acc)[4][2]) const
+    {
+        u32x4 fa[2][4], fb[2][2];
+        const auto read_frags = [&](int h) {
+            const int even = h & ~1, odd = h & 1;
+            const uint32_t pa = (uint32_t)(LA == LINES ? (even + GRP) % 5 : h % 5) * kPiece;
+            const uint32_t pb =
+                B_BASE + (uint32_t)(LB == LINES ? (even + (q >> 1)) % 5 : h & 3) * kPiece;
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                    fa[st][i] = LA == LINES ? read_line(pa, a_line, odd, st, i) : read_tr(pa, a_tr[i], st);
+#pragma unroll
+                for (int i = 0; i < (NB ? 2 : 0); ++i)
+                    fb[st][i] = LB == LINES ? read_line(pb, b_line, odd, st, i) : read_tr(pb, b_tr[i], st);
+            }
+        };
+        const auto multiply = [&]() {
+#pragma unroll
+            for (int st = 0; st < 2; ++st)
+#pragma unroll
+                for (int i = 0; i < 2 * NB; ++i)
+                    mfma16<DT>(acc[i >> 1][i & 1], fb[st][i & 1], fa[st][i >> 1]);
+        };
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i)
+            acc[i >> 1][i & 1] = f32x16{};
+        const int n = (k + 31) / 32;
+        if (n > 0) {
             phase_end();
-            if (h + 1 < n) {
-                copy_piece(h + 4);
-                read_frags(h + 1);
+            if constexpr (GRP == 0) {
+                copy_piece(3);
+                read_frags(0);
             }
             phase_end();
-        } else {
-            copy_piece(h + 3);
-            read_frags(h);
-            phase_end();
-            multiply();
-            phase_end();
         }
+        for (int h = 0; h < n; ++h) {
+            if constexpr (GRP == 0) {
+                multiply();
+                phase_end();
+                if (h + 1 < n) {
+                    copy_piece(h + 4);
+                    read_frags(h + 1);
+                }
+                phase_end();
+            } else {
+                copy_piece(h + 3);
+                read_frags(h);
+                phase_end();
+                multiply();
+                phase_end();
+            }
+        }
+        wait_vmcnt<0>();  // the zero-filling copies past the end
     }
-    wait_vmcnt<0>();  // the zero-filling copies past the end
+};
+
+// One tile per workgroup: calls f(accumulators, blocks, first row, first
+// column) in every wave once its sums are complete; 32-row blocks 0 .. blocks -
+// 1 (a compile-time constant) hold sums.  The wave groups and block counts have
+// code of their own, so no accumulator is merged between paths.
+template <int DT, int LA, int LB, int GRP, typename F>
+__device__ __forceinline__ void big_tile_group(const TileWork &w, uint8_t *lds, int q, F &&f)
+{
+    BigGroup<DT, LA, LB, GRP> group(lds, q);
+    f32x16 acc[4][2];
+    group.set(w);
+    group.start();
+    const auto run = [&](auto nb) {
+        group.template run<decltype(nb)::value>(acc);
+        f(acc, nb, GRP * 128, q * 64);
+    };
+    if (w.m > GRP * 128 + 64)
+        run(IC<4>{});
+    else if (w.m > GRP * 128)
+        run(IC<2>{});
+    else if constexpr (GRP == 1)  // (a tile has a row)
+        run(IC<0>{});
 }
 
-// Calls f(accumulators, blocks, first row, first column) in every wave once
-// the tile's sums are complete: 32-row blocks 0 .. blocks - 1 (a compile-time
-// constant) hold sums.  A group's last tile is often a low one; its empty
-// blocks are not multiplied (2 or 4 blocks per group, or none), each case in
-// code of its own: branches inside the bursts would have the accumulators
-// spilled.  The wave groups have their own copies of everything too, so no
-// register value is merged between paths.
 template <int DT, int LA, int LB, typename F>
 __device__ __forceinline__ void big_tile(const TileWork &w, uint8_t *lds, F &&f)
 {
     // wave index as a scalar: the branches are uniform
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    f32x16 acc[4][2];
-    if (wave < 4) {
-        if (w.m > 64) {
-            big_tile_group<DT, LA, LB, 0, 4>(acc, w, lds, wave);
-            f(acc, IC<4>{}, 0, wave * 64);
-        } else {
-            big_tile_group<DT, LA, LB, 0, 2>(acc, w, lds, wave);
-            f(acc, IC<2>{}, 0, wave * 64);
+    if (wave < 4)
+        big_tile_group<DT, LA, LB, 0>(w, lds, wave, f);
+    else
+        big_tile_group<DT, LA, LB, 1>(w, lds, wave - 4, f);
+}
+
+// ---- many tiles per workgroup
+//
+// A tile of depth 2048 takes about 50 us of products, and some 13 us more were
+// spent around them by a workgroup per tile: its dispatch, finding its place,
+// the first copies' latency, the stores.  So a workgroup per CU stays and takes
+// tiles from queues, one per die, each a contiguous run of tile numbers (an
+// empty queue's workgroups help the others out); the next tile's first copies
+// are issued before this one's stores, and its number is asked for a tile
+// ahead.  Which workgroup computes a tile changes nothing in it.
+constexpr int kQueues = 8;
+
+struct TileQueues {
+    int32_t first[kQueues]; // the first tiles go to the queue's workgroups in turn,
+    int32_t next[kQueues];  // and from here on to whoever asks
+    int32_t end[kQueues];
+};
+
+// Queue x: tiles [begin, end), for a launch of `workgroups`.
+__device__ __forceinline__ void fill_queue(TileQueues *queues, int x, int begin, int end, int workgroups)
+{
+    const int mine = (workgroups - x + kQueues - 1) / kQueues;
+    queues->first[x] = begin;
+    queues->next[x] = begin + mine < end ? begin + mine : end;
+    queues->end[x] = end;
+}
+
+// A tile of queue *x or, if that is empty, of the nearest one that is not; -1
+// when all are.  By one wave: its lanes look at all queues at once (an add to a
+// queue that many workgroups find empty takes microseconds).  Every round
+// either takes a tile or finds a queue emptied, so the rounds end.
+__device__ __forceinline__ int take_tile(TileQueues *queues, int *x)
+{
+    const int lane = threadIdx.x & 63, at = (*x + lane) % kQueues;
+    for (;;) {
+        const int next = __hip_atomic_load(&queues->next[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint64_t some = __builtin_amdgcn_ballot_w64(lane < kQueues && next < queues->end[at]);
+        if (!some)
+            return -1;
+        const int first = __builtin_ctzll(some);
+        int id = 0, end = 0;
+        if (lane == first) {
+            id = __hip_atomic_fetch_add(&queues->next[at], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            end = queues->end[at];
         }
-    } else if (w.m > 192) {
-        big_tile_group<DT, LA, LB, 1, 4>(acc, w, lds, wave - 4);
-        f(acc, IC<4>{}, 128, (wave - 4) * 64);
-    } else if (w.m > 128) {
-        big_tile_group<DT, LA, LB, 1, 2>(acc, w, lds, wave - 4);
-        f(acc, IC<2>{}, 128, (wave - 4) * 64);
-    } else {
-        big_tile_group<DT, LA, LB, 1, 0>(acc, w, lds, wave - 4);
-        f(acc, IC<0>{}, 128, (wave - 4) * 64);
+        id = __builtin_amdgcn_readlane(id, first);
+        if (id < __builtin_amdgcn_readlane(end, first)) {
+            *x = __builtin_amdgcn_readlane(at, first);
+            return id;
+        }
     }
+}
+
+// Where a tile's sums go: C at the tile's first row, its first column, and how
+// many rows from there on exist.
+struct TilePlace {
+    uint8_t *c;
+    int n0, m;
+};
+
+// tiles(id, &work, &place) describes a tile; store(acc, blocks, place, row,
+// col) puts a wave's sums where they belong (as f of big_tile).
+template <int DT, int LA, int LB, int GRP, typename Tiles, typename Store>
+__device__ __forceinline__ void big_tiles_group(TileQueues *queues, uint8_t *lds, int q, Tiles &&tiles,
+                                                Store &&store)
+{
+    BigGroup<DT, LA, LB, GRP> group(lds, q);
+    const bool asks = GRP == 0 && q == 0;  // one wave
+    // the tile number passes through a place in LDS that the next tile's first
+    // copies do not reach (piece 3 of B's ring is first filled two barriers
+    // after everyone has read it)
+    volatile int32_t *const pass =
+        (volatile int32_t *)(lds + BigGroup<DT, LA, LB, GRP>::B_BASE + 3 * kPiece);
+    int x = (int)blockIdx.x % kQueues;
+    int id = queues->first[x] + (int)blockIdx.x / kQueues;
+    if (id >= queues->end[x]) {  // (fewer tiles than workgroups)
+        if (asks) {
+            id = take_tile(queues, &x);
+            *pass = id;
+        }
+        wait_lds();
+        barrier_only();
+        id = __builtin_amdgcn_readfirstlane(*pass);
+        if (id < 0)
+            return;
+    }
+    TileWork w;
+    TilePlace place;
+    tiles(id, &w, &place);
+    group.set(w);
+    group.start();
+    int ahead, end;
+    const auto ask = [&]() {
+        if (asks) {
+            if ((threadIdx.x & 63) == 0)
+                ahead = __hip_atomic_fetch_add(&queues->next[x], 1, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
+            end = queues->end[x];
+        }
+    };
+    ask();
+    f32x16 acc[4][2];
+    while (true) {
+        const TilePlace here = place;
+        const auto run = [&](auto nb) {
+            constexpr int NB = decltype(nb)::value;
+            group.template run<NB>(acc);
+            barrier_only();  // everybody is done with the rings
+            if (asks) {
+                // asked for a tile ago
+                int mine = __builtin_amdgcn_readfirstlane(ahead);
+                if (mine >= __builtin_amdgcn_readfirstlane(end))
+                    mine = take_tile(queues, &x);
+                *pass = mine;
+            }
+            wait_lds();
+            barrier_only();
+            id = __builtin_amdgcn_readfirstlane(*pass);
+            if (id >= 0) {
+                tiles(id, &w, &place);
+                group.set(w);
+                group.start();
+                ask();
+            }
+            store(acc, nb, here, GRP * 128, q * 64);
+        };
+        if (here.m > GRP * 128 + 64)
+            run(IC<4>{});
+        else if (GRP == 0 || here.m > GRP * 128)
+            run(IC<2>{});
+        else
+            run(IC<0>{});
+        if (id < 0)
+            return;
+    }
+}
+
+// 4 KiB per wave that a tile's stores may use while the next tile's first copies
+// are on their way: pieces 3 and 4 of A's ring.
+__device__ __forceinline__ uint8_t *store_lds(uint8_t *lds)
+{
+    return lds + 3 * kPiece + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * 4096;
+}
+
+template <int DT, int LA, int LB, typename Tiles, typename Store>
+__device__ __forceinline__ void big_tiles(TileQueues *queues, uint8_t *lds, Tiles &&tiles, Store &&store)
+{
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    if (wave < 4)
+        big_tiles_group<DT, LA, LB, 0>(queues, lds, wave, tiles, store);
+    else
+        big_tiles_group<DT, LA, LB, 1>(queues, lds, wave - 4, tiles, store);
 }
 
 // ---------------------------------------------------------------------------
