@@ -2,6 +2,7 @@
 import os
 import shutil
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,17 +22,25 @@ def hipcc():
 
 
 def build(out=LIB, verbose=False, extra=()):
-    """Compile every source for gfx950 into one shared library; returns its path."""
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-           f"-I{INCLUDE}", f"-I{CSRC}",
-           # packed fp32 VALU ops are kept out of the generated code
-           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-           *extra, *SOURCES, "-o", out + ".tmp"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    """Compile every source for gfx950, side by side, into one shared library;
+    returns its path."""
+    flags = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", f"-I{INCLUDE}", f"-I{CSRC}",
+             # packed fp32 VALU ops are kept out of the generated code
+             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", *extra]
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, os.path.basename(s) + ".o") for s in SOURCES]
+        jobs = [subprocess.Popen([hipcc(), *flags, "-c", s, "-o", o], stdout=subprocess.DEVNULL,
+                                 stderr=subprocess.PIPE, text=True)
+                for s, o in zip(SOURCES, objs)]
+        errs = [job.communicate()[1] for job in jobs]
+        if any(job.returncode for job in jobs):
+            raise RuntimeError("hipcc failed:\n" + "\n".join(errs)[-8000:])
+        res = subprocess.run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o",
+                              out + ".tmp"], capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("hipcc failed:\n" + res.stderr[-8000:])
     if verbose:
-        print(res.stderr)
+        print("\n".join(errs) + res.stderr)
     os.replace(out + ".tmp", out)
     return out
 

@@ -136,6 +136,25 @@ __device__ __forceinline__ u32x4 load_some(const T *p, int n)
 // launch.
 constexpr int shrink_waves(int rt, int rb) { return rt * rb <= 4 ? 16 : 64 / (rt * rb); }
 
+// sum[ranks 4 q .. + 3][row] += one step of a 16-rank block by a 16-row block
+template <int DT>
+__device__ __forceinline__ void rank_step(f32x4 &sum, u32x4 ranks, u32x4 rows)
+{
+    if constexpr (DT == 1) {
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, ranks),
+                                                     __builtin_bit_cast(f16x8, rows), sum, 0, 0, 0);
+    } else if constexpr (DT == 2) {
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ranks),
+                                                      __builtin_bit_cast(bf16x8, rows), sum, 0, 0, 0);
+    } else {
+        // element e of both operands: the same k meets the same k
+        const f32x4 a = as_floats(ranks), x = as_floats(rows);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            sum = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], x[e], sum, 0, 0, 0);
+    }
+}
+
 template <int DT, int RT, int RB>  // RT: 16-rank blocks, RB: 16-row blocks
 __global__ __launch_bounds__(64 * shrink_waves(RT, RB)) void shrink_kernel(AdapterArgs a)
 {
@@ -204,25 +223,8 @@ __global__ __launch_bounds__(64 * shrink_waves(RT, RB)) void shrink_kernel(Adapt
 #pragma unroll
             for (int b = 0; b < RB; ++b)
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    if constexpr (DT == 1) {
-                        acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            __builtin_bit_cast(f16x8, fa[t]), __builtin_bit_cast(f16x8, fx[b]),
-                            acc[b][t], 0, 0, 0);
-                    } else if constexpr (DT == 2) {
-                        acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, fa[t]), __builtin_bit_cast(bf16x8, fx[b]),
-                            acc[b][t], 0, 0, 0);
-                    } else {
-                        // element e of both operands: the same k meets the same k
-                        const f32x4 af = __builtin_bit_cast(f32x4, fa[t]);
-                        const f32x4 xf = __builtin_bit_cast(f32x4, fx[b]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(af[e], xf[e], acc[b][t],
-                                                                             0, 0, 0);
-                    }
-                }
+                for (int t = 0; t < RT; ++t)
+                    rank_step<DT>(acc[b][t], fa[t], fx[b]);
         };
         int k = k0;
         for (; k + kAhead * 4 * V <= k1; k += kAhead * 4 * V) {
@@ -460,8 +462,8 @@ __device__ __forceinline__ void add_adapters(f32x16 (&acc)[MT ? MT : 1][NT], con
                                     // ranks 8 half + e of both operands meet in instruction e
 #pragma unroll
                                     for (int e = 0; e < 8; ++e) {
-                                        const f32x4 x = __builtin_bit_cast(f32x4, fb[g][j][e >> 2]);
-                                        const f32x4 y = __builtin_bit_cast(f32x4, fh[e >> 2]);
+                                        const f32x4 x = as_floats(fb[g][j][e >> 2]);
+                                        const f32x4 y = as_floats(fh[e >> 2]);
                                         sum = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e & 3], y[e & 3], sum,
                                                                                    0, 0, 0);
                                     }
@@ -614,7 +616,7 @@ __device__ __forceinline__ bool join_parts(f32x16 (&acc)[MT][NT], const AdapterA
         for (int p = 0; p < kTogether; ++p)
 #pragma unroll
             for (int i = 0; i < kQuads; ++i) {
-                const f32x4 f = __builtin_bit_cast(f32x4, v[p][i]);
+                const f32x4 f = as_floats(v[p][i]);
                 f32x16 &x = acc[i / 4 / NT][i / 4 % NT];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)

@@ -39,6 +39,8 @@ __device__ __forceinline__ uint32_t bf16_bits(float x)
     return __builtin_bit_cast(uint16_t, (__bf16)x);
 }
 
+__device__ __forceinline__ f32x4 as_floats(u32x4 x) { return __builtin_bit_cast(f32x4, x); }
+
 // Four consecutive columns n .. n + 3 of a row of C, at byte offset `row_off`
 // of the descriptor's base; ok: the row is inside C.  c_dtype: 0 fp32, 1 fp16,
 // 2 bf16, rounded to nearest even from the fp32 sums.  vec (uniform): the four

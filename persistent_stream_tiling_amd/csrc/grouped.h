@@ -62,7 +62,7 @@ struct RowTile {
 // turn), so a group's matrix is read into one die's L2, or two.  False: no
 // tile for this workgroup.
 template <int BM>
-__device__ __forceinline__ bool find_row_tile(const GroupedArgs &a, int64_t hw, RowTile *out)
+__device__ __forceinline__ bool find_row_tile(const GroupedArgs &a, int32_t hw, RowTile *out)
 {
     const int lane = threadIdx.x & 63;
     const int32_t runs = a.groups + 1;  // with the rows past the last group
@@ -81,15 +81,18 @@ __device__ __forceinline__ bool find_row_tile(const GroupedArgs &a, int64_t hw, 
         const int32_t up = __shfl_up(sum, d);
         sum += lane >= d ? up : 0;
     }
-    const int64_t total = (int64_t)__builtin_amdgcn_readlane(sum, 63) * a.tiles_n;
-    const int64_t share = (total + a.xcds - 1) / a.xcds;
-    const int64_t die = hw % a.xcds, nth = hw / a.xcds;
-    const int64_t id = die * share + nth;
+    // (a launch has fewer than 2^24 workgroups; offsets that do not ascend can
+    // make the sums larger, or wrap)
+    const int64_t tiles = (int64_t)__builtin_amdgcn_readlane(sum, 63) * a.tiles_n;
+    const int32_t total = tiles < 0 ? 0 : (tiles < (1 << 30) ? (int32_t)tiles : 1 << 30);
+    const int32_t share = (total + a.xcds - 1) / a.xcds;
+    const int32_t die = hw % a.xcds, nth = hw / a.xcds;
+    const int32_t id = die * share + nth;
     if (nth >= share || id >= total)
         return false;
-    const int32_t rt = (int32_t)(id / a.tiles_n);
+    const int32_t rt = id / a.tiles_n;
     const uint64_t past = __builtin_amdgcn_ballot_w64(sum > rt);
-    if (!past)  // (offsets that do not ascend can make the sums wrap)
+    if (!past)
         return false;
     const int owner = __builtin_ctzll(past);
     // the owner lane walks its groups; every lane follows with its values
@@ -105,7 +108,7 @@ __device__ __forceinline__ bool find_row_tile(const GroupedArgs &a, int64_t hw, 
     out->g = g;
     out->m0 = lo + (rt - at) * BM;
     out->m_end = hi;
-    out->tn = (int32_t)(id - (int64_t)rt * a.tiles_n);
+    out->tn = id - rt * a.tiles_n;
     return true;
 }
 

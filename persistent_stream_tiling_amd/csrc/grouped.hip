@@ -36,7 +36,7 @@ __global__ __launch_bounds__(kXThreads, 2) void rows_exact_kernel(GroupedArgs a)
 {
     __shared__ __attribute__((aligned(16))) float lds[4 * kXDeep * kXPitch];
     RowTile t;
-    if (!find_row_tile<kXTile>(a, blockIdx.x, &t))
+    if (!find_row_tile<kXTile>(a, (int32_t)blockIdx.x, &t))
         return;
     const int n0 = t.tn * kXTile, m = t.m_end - t.m0 < kXTile ? t.m_end - t.m0 : kXTile;
     // (the rows past the last group multiply nothing: depth 0)
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(256, 2) void rows_narrow_kernel(GroupedArgs a)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[narrow_lds(MT)];
     RowTile t;
-    if (!find_row_tile<32 * MT>(a, blockIdx.x, &t))
+    if (!find_row_tile<32 * MT>(a, (int32_t)blockIdx.x, &t))
         return;
     const int n0 = t.tn * kNarrow;
     const TileWork w = rows_work<LB>(a, t, n0);

@@ -1,0 +1,116 @@
+"""A mixture-of-experts layer on the operators of ``rows``, trained by explicit
+gradients, and served with a low-rank adapter per request (GPU).
+
+  python -m persistent_stream_tiling_amd.expert_layer --steps 30
+
+``ExpertLayer`` routes each token to its best ``choices`` of ``experts``
+two-layer networks (relu between), weights their outputs with the softmax of
+the chosen scores, and returns every gradient from ``backward``.  The command
+fits such a layer to a seeded target, then projects its output for requests
+that each carry their own adapter.
+"""
+import argparse
+
+import torch
+
+from .rows import (adapter_matmul, combine_rows, combine_rows_backward, gather_rows,
+                   gather_rows_backward, grouped_matmul, grouped_matmul_wgrad, route_rows)
+
+
+class ExpertLayer:
+    """y[t] = sum over t's chosen experts e of p[t, e] * relu(x[t] @ up[e]) @ down[e],
+    p the softmax of the chosen experts' scores x[t] @ router.  Weights are fp32
+    masters; products run in ``dtype``."""
+
+    def __init__(self, width, hidden, experts, choices, dtype=torch.bfloat16, seed=0,
+                 device="cuda"):
+        gen = torch.Generator(device=device).manual_seed(seed)
+
+        def normal(*shape):
+            return torch.randn(shape, generator=gen, device=device) * shape[-2] ** -0.5
+
+        self.choices, self.experts, self.dtype = choices, experts, dtype
+        self.weights = {"router": normal(width, experts), "up": normal(experts, width, hidden),
+                        "down": normal(experts, hidden, width)}
+
+    def forward(self, x):
+        """y (tokens x width) in the layer's dtype; keeps what backward needs."""
+        w = {k: v.to(self.dtype) for k, v in self.weights.items()}
+        scores = x.float() @ self.weights["router"]
+        top, ids = torch.topk(scores, self.choices, dim=1)
+        p = torch.softmax(top, dim=1)
+        r = route_rows(ids, self.experts)
+        xs = gather_rows(x, r)
+        h = grouped_matmul(xs, w["up"], r.offsets, out_dtype=self.dtype)
+        a = torch.relu(h)
+        ys = grouped_matmul(a, w["down"], r.offsets, out_dtype=self.dtype)
+        self.kept = (x, w, ids, p, r, xs, h, a, ys)
+        return combine_rows(ys, p, r)
+
+    def backward(self, dy):
+        """The gradients of the weights (fp32, by name) and of x."""
+        x, w, ids, p, r, xs, h, a, ys = self.kept
+        dys, dp = combine_rows_backward(dy, ys, p, r)
+        grads = {"down": grouped_matmul_wgrad(a, dys, r.offsets)}
+        da = grouped_matmul(dys, w["down"].transpose(1, 2), r.offsets, out_dtype=self.dtype)
+        dh = da * (h > 0)
+        grads["up"] = grouped_matmul_wgrad(xs, dh, r.offsets)
+        dxs = grouped_matmul(dh, w["up"].transpose(1, 2), r.offsets, out_dtype=self.dtype)
+        dx = gather_rows_backward(dxs, r)
+        # softmax over the chosen scores, scattered back to all experts
+        dtop = p * (dp - (dp * p).sum(1, keepdim=True))
+        dscores = torch.zeros(x.shape[0], self.experts, device=x.device).scatter_(1, ids, dtop)
+        grads["router"] = x.float().t() @ dscores
+        return grads, (dx.float() + dscores @ self.weights["router"].t()).to(self.dtype)
+
+
+def fit(steps=30, tokens=512, width=256, hidden=384, experts=8, choices=2, lr=0.1, seed=0,
+        log=print):
+    """Fit a layer to another one's outputs; returns the layer, its inputs and
+    the mean squared errors."""
+    gen = torch.Generator(device="cuda").manual_seed(seed + 1)
+    layer = ExpertLayer(width, hidden, experts, choices, seed=seed)
+    target = ExpertLayer(width, hidden, experts, choices, seed=seed + 2)
+    x = torch.randn(tokens, width, generator=gen, device="cuda").to(layer.dtype)
+    want = target.forward(x).float()
+    errors = []
+    for step in range(steps):
+        diff = layer.forward(x).float() - want
+        errors.append(float((diff ** 2).mean()))
+        grads, _ = layer.backward((diff * (2.0 / tokens)).to(layer.dtype))
+        for name, g in grads.items():
+            layer.weights[name] -= lr * g
+        if log and step % 10 == 0:
+            log(f"step {step}: mean squared error {errors[-1]:.5f}")
+    return layer, x, errors
+
+
+def serve(layer, x, requests=32, rank=16, seed=0):
+    """The layer's output for the first ``requests`` tokens, projected by one
+    shared linear layer with each request's own adapter."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    width, dt = x.shape[1], layer.dtype
+
+    def normal(*shape):
+        return (torch.randn(shape, generator=gen, device="cuda") * shape[-1] ** -0.5).to(dt)
+
+    w, a, b = normal(width, width), normal(requests, rank, width), normal(requests, width, rank)
+    ids = torch.arange(requests, dtype=torch.int32, device="cuda")
+    ids[::5] = -1  # every fifth request has none
+    y = layer.forward(x[:requests])
+    return adapter_matmul(y, w.t(), a, b, ids, out_dtype=dt), (y, w, a, b, ids)
+
+
+def main(argv=None):
+    ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    ap.add_argument("--steps", type=int, default=30)
+    ap.add_argument("--tokens", type=int, default=512)
+    args = ap.parse_args(argv)
+    layer, x, errors = fit(args.steps, args.tokens)
+    print(f"mean squared error {errors[0]:.5f} -> {errors[-1]:.5f} in {args.steps} steps")
+    out, _ = serve(layer, x)
+    print(f"served {out.shape[0]} requests: {tuple(out.shape)} {out.dtype}")
+
+
+if __name__ == "__main__":
+    main()

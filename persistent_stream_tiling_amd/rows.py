@@ -16,8 +16,9 @@ and its gradients from ``dy``:
     dxs = grouped_matmul(dys, w.transpose(1, 2), r.offsets, out_dtype=x.dtype)
     dx = gather_rows_backward(dxs, r)
 
-Nothing here reads the GPU: group sizes stay there, and every call can be
-captured into a graph.  Outputs and workspaces come from torch's allocator on
+Nothing here waits for the GPU: group sizes stay there, and every call can be
+captured into a graph.  The calls record nothing for autograd: gradients are
+the explicit calls above.  Outputs and workspaces come from torch's allocator on
 the current stream, which is the stream each call runs on; tensors made on
 another stream need that stream's usual synchronization and
 ``record_stream``.
@@ -53,6 +54,13 @@ class Routing:
                 self.order.shape != (self.position.numel(),):
             raise ValueError("a routing holds offsets (groups + 1), order (tokens * choices) and "
                              "position (tokens x choices)")
+
+    @classmethod
+    def _made(cls, offsets, order, position):
+        """A routing that this module made: nothing to check."""
+        self = object.__new__(cls)
+        self.__dict__.update(offsets=offsets, order=order, position=position)
+        return self
 
     @property
     def groups(self):
@@ -128,7 +136,7 @@ def route_rows(ids, groups):
     ws = _bytes(lib.gemm_route_workspace_size(T, k, groups), dev)
     _call(dev, lib.gemm_route, ids.data_ptr(), ids.element_size(), T, k, groups,
           offsets.data_ptr(), order.data_ptr(), position.data_ptr(), _ptr(ws))
-    return Routing(offsets, order, position)
+    return Routing._made(offsets, order, position)
 
 
 def _rows(what, t, n, cols=None):

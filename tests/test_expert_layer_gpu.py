@@ -1,0 +1,52 @@
+"""The mixture-of-experts example: its gradients against autograd in 64 bits,
+its fit, and its served projection."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+from persistent_stream_tiling_amd.expert_layer import ExpertLayer, fit, serve  # noqa: E402
+
+
+def test_gradients_against_autograd():
+    # fp32 products: what the layer computes, differentiated by autograd on the CPU
+    layer = ExpertLayer(40, 56, 6, 2, dtype=torch.float32, seed=3)
+    x = torch.randn(70, 40, generator=torch.Generator().manual_seed(1))
+    dy = torch.randn(70, 40, generator=torch.Generator().manual_seed(2))
+    y = layer.forward(x.cuda())
+    grads, dx = layer.backward(dy.cuda())
+    w = {k: v.double().cpu().requires_grad_() for k, v in layer.weights.items()}
+    X = x.double().requires_grad_()
+    top, ids = torch.topk(X @ w["router"], 2, dim=1)
+    assert torch.equal(ids, layer.kept[2].cpu())
+    p = torch.softmax(top, dim=1)
+    rows = []
+    for t in range(70):
+        rows.append(sum(p[t, j] * (torch.relu(X[t] @ w["up"][e]) @ w["down"][e])
+                        for j, e in enumerate(ids[t].tolist())))
+    Y = torch.stack(rows)
+    Y.backward(dy.double())
+    # sums of at most 70 products in fp32, a few of them one after the other
+    for got, want in [(y, Y.detach()), (dx, X.grad)] + [(grads[k], w[k].grad) for k in w]:
+        scale = float(want.abs().max())
+        assert float((got.double().cpu() - want).abs().max()) <= 2000 * 2.0 ** -24 * scale
+
+
+def test_the_layer_fits_its_target():
+    _, _, errors = fit(steps=25, log=None)
+    assert errors[-1] < 0.5 * errors[0]
+
+
+def test_served_rows_have_their_adapters():
+    layer, x, _ = fit(steps=1, log=None)
+    out, (y, w, a, b, ids) = serve(layer, x)
+    Y, W, A, B = (t.double() for t in (y, w, a, b))
+    want = Y @ W.T
+    for t, g in enumerate(ids.tolist()):
+        if g >= 0:
+            want[t] += B[g] @ (A[g] @ Y[t])
+    # half a step of bf16, and the fp32 sums below it
+    assert bool(((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-3 * want.abs().max()).all())

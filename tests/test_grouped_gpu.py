@@ -172,6 +172,68 @@ def test_offsets_out_of_range_or_order_touch_nothing_else():
     within(c, ref, 2 * K * U * size)
 
 
+def spread(groups, seed, most):
+    """Group sizes of very different lengths, some of them zero."""
+    rng = np.random.default_rng(seed)
+    n = np.floor(most * rng.random(groups) ** 3).astype(int)
+    n[rng.random(groups) < 0.15] = 0
+    return n.tolist()
+
+
+@pytest.mark.parametrize("trans", [False, True], ids=["b", "bT"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_more_tiles_than_workgroups(trans, dtype):
+    # hundreds of 256x256 tiles of very different depth of work: every
+    # workgroup takes several, and the queues run empty at different times
+    check_rows(spread(20, 3, 3000), 700, 72, 1032, dtype, True, trans)
+    check_rows([256] * 90 + [0, 1, 255, 257], 5, 40, 1096, dtype, False, trans)
+    # fewer tiles than workgroups, and fewer than queues
+    check_rows([300, 500], 0, 264, 300, dtype, True, trans)
+    check_rows([1000], 0, 64, 100, dtype, True, trans)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_weight_gradient_of_many_groups(dtype):
+    check_wgrad(spread(45, 5, 900), 30, 520, 776, dtype, False)
+    check_wgrad(spread(45, 6, 900), 0, 300, 1100, dtype, True)
+    # more groups than are sorted by size; and the most there can be
+    check_wgrad([i % 4 for i in range(1100)], 3, 24, 40, dtype, False)
+    check_wgrad([i % 2 for i in range(4096)], 0, 8, 16, dtype, True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_most_groups(dtype):
+    check_rows([i % 3 for i in range(4096)], 7, 24, 40, dtype, False, False)
+    check_rows([0] * 4095 + [2000], 7, 24, 40, dtype, False, True)
+
+
+@pytest.mark.parametrize("mean", [1, 400])
+def test_rows_past_32_bit_offsets(mean):
+    # A beyond 4 GiB, on the tiles of few and of many rows: the last groups
+    K, N = 4096, 40
+    rows = 560_000
+    G = min(rows // mean, 4096)
+    sizes = [mean] * (G - 1)
+    off = offsets_of(sizes + [rows - sum(sizes)])
+    a = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    tail = normal((300, K), "bf16", 1)
+    a[-300:] = tail.cuda()
+    b = normal((G, K, N), "bf16", 2) if G < 1500 else normal((1, K, N), "bf16", 2).expand(G, K, N)
+    c = gsk.grouped_matmul(a, b.cuda(), torch.from_numpy(off).to(torch.int32).cuda())
+    g_of = np.searchsorted(off, np.arange(rows - 300, rows), side="right") - 1
+    ref, size = np.zeros((300, N)), np.zeros((300, N))
+    for g in np.unique(g_of):
+        m = g_of == g
+        B = f64(b[g])
+        ref[m], size[m] = f64(tail)[m] @ B, np.abs(f64(tail)[m]) @ np.abs(B)
+    within(c[-300:], ref, 2 * K * U * size)
+    assert (c[:1000] == 0).all()
+    w = gsk.grouped_matmul_wgrad(a, a[:, :N].contiguous(), torch.from_numpy(off).to(torch.int32).cuda())
+    m = f64(tail)[g_of == G - 1]
+    ref, size = m.T @ m[:, :N], np.abs(m).T @ np.abs(m[:, :N])
+    within(w[G - 1], ref, 2 * rows * U * size)
+
+
 def test_strided_inputs_are_taken_as_they_are():
     off = torch.tensor([0, 70, 130], dtype=torch.int32, device="cuda")
     a, b = normal((260, 80), "f16", 1).cuda(), normal((4, 80, 96), "f16", 2).cuda()

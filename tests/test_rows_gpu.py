@@ -182,6 +182,22 @@ def test_more_tokens_than_one_launch_holds():
     assert bool(((dw.double() - ref).abs() <= 2 * (cols + 1) * U * ref).all())
 
 
+def test_rows_past_32_bit_offsets():
+    # sorted rows beyond 4 GiB
+    tokens, choices, cols = 290_000, 8, 1024
+    ids = torch.randint(0, 16, (tokens, choices), dtype=torch.int32, device="cuda")
+    r = gsk.route_rows(ids, 16)
+    x = torch.randn(tokens, cols, device="cuda").to(torch.bfloat16)
+    xs = gsk.gather_rows(x, r)
+    last = torch.arange(tokens * choices - 5000, tokens * choices, device="cuda")
+    assert torch.equal(xs[last], x[r.order[last].long() // choices])
+    w = torch.ones(tokens, choices, device="cuda")
+    y = gsk.combine_rows(xs, w, r)  # eight times x, exactly
+    assert torch.equal(y, x * 8)
+    dys, dw = gsk.combine_rows_backward(x, xs, w, r)
+    assert torch.equal(dys[last], xs[last])
+
+
 def test_same_bits_on_another_stream_and_again():
     ids = random_ids(700, 4, 30, 0.1, 3).cuda()
     ys, w = normal((2800, 333), "bf16", 1).cuda(), normal((700, 4), "f32", 2).cuda()
