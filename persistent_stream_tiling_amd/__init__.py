@@ -21,7 +21,8 @@ def __getattr__(name):
     # these need torch, which the planning and inspection calls do without
     if name in _ROWS:
         from . import rows
-        return getattr(rows, name)
+        globals().update((n, getattr(rows, n)) for n in _ROWS)
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -222,14 +222,26 @@ struct Row16 {
     typedef T Elements __attribute__((ext_vector_type(16 / sizeof(T))));
 };
 
+// Sorted rows past the size of the caches are read and written with the
+// non-temporal hint: their lines are used once.  Measured with and without, by
+// the size of the sorted rows: 268 MB gather 65.0 / 72.3 us, 268 MB sum 52.5 /
+// 60.6 us, 134 MB gradient of a sum 65.0 / 70.9 us; but 69 MB, which the last
+// cache still held, 20.9 / 17.0 us.
+constexpr int64_t kStreamBytes = (int64_t)100 << 20;
+
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 // The elements of a row from column c, those past `cols` as zero.
-template <typename T>
+template <bool STREAM = false, typename T>
 __device__ __forceinline__ u32x4 load_vec(const T *row, int c, int cols)
 {
     constexpr int V = Row16<T>::V;
     u32x4 w;
     if (c + V <= cols) {
-        __builtin_memcpy(&w, row + c, 16);
+        if constexpr (STREAM)
+            w = __builtin_nontemporal_load((const u32x4_any *)(row + c));
+        else
+            __builtin_memcpy(&w, row + c, 16);
     } else {
         T x[V];
 #pragma unroll
@@ -240,12 +252,15 @@ __device__ __forceinline__ u32x4 load_vec(const T *row, int c, int cols)
     return w;
 }
 
-template <typename T>
+template <bool STREAM = false, typename T>
 __device__ __forceinline__ void store_vec(T *row, int c, int cols, u32x4 w)
 {
     constexpr int V = Row16<T>::V;
     if (c + V <= cols) {
-        __builtin_memcpy(row + c, &w, 16);
+        if constexpr (STREAM)
+            __builtin_nontemporal_store(w, (u32x4_any *)(row + c));
+        else
+            __builtin_memcpy(row + c, &w, 16);
     } else {
         T x[V];
         __builtin_memcpy(x, &w, 16);
@@ -307,7 +322,7 @@ __device__ __forceinline__ void load_rows(int32_t (&row)[J], const int32_t *posi
 // xs[position[t][j]] = x[t] for every choice j; rows past the kept ones are
 // zeroed (row e = t * choices + j by token t: rows and entries count alike).
 // J: choices per round.  Bound by the writes, choices rows for each row read.
-template <typename T, int J>
+template <typename T, int J, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void gather_kernel(const T *__restrict__ x,
                                                              const int32_t *__restrict__ position,
                                                              const int32_t *__restrict__ kept,
@@ -329,10 +344,10 @@ __global__ __launch_bounds__(kRowThreads) void gather_kernel(const T *__restrict
 #pragma unroll
             for (int j = 0; j < J; ++j)
                 if (row[j] >= 0)
-                    store_vec(xs + (int64_t)row[j] * g.cols, c, g.cols, v);
+                    store_vec<STREAM>(xs + (int64_t)row[j] * g.cols, c, g.cols, v);
         }
         for (int64_t e = e0 > live ? e0 : live; e < e0 + g.choices; ++e)
-            store_vec(xs + e * g.cols, c, g.cols, u32x4{});
+            store_vec<STREAM>(xs + e * g.cols, c, g.cols, u32x4{});
     }
 }
 
@@ -341,7 +356,7 @@ __global__ __launch_bounds__(kRowThreads) void gather_kernel(const T *__restrict
 // that all J of a round are in flight together, and are then ignored).
 // Without weights: the plain sum, which is the gradient of gather_kernel.
 // Bound by the reads of the sorted rows.
-template <typename T, bool WEIGHTS, int J>
+template <typename T, bool WEIGHTS, int J, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(const T *__restrict__ ys,
                                                               const int32_t *__restrict__ position,
                                                               const float *__restrict__ weights,
@@ -367,7 +382,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(const T *__restric
                 w[j] = WEIGHTS ? weights[e0 + (j0 + j < g.choices ? j0 + j : 0)] : 1.0f;
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                v[j] = load_vec(ys + (int64_t)(row[j] >= 0 ? row[j] : 0) * g.cols, c, g.cols);
+                v[j] = load_vec<STREAM>(ys + (int64_t)(row[j] >= 0 ? row[j] : 0) * g.cols, c, g.cols);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 float x[V];
@@ -388,7 +403,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(const T *__restric
 // pass over ys; rows of dys past the kept ones are zeroed.  The dot products
 // are summed per lane over its columns, then over the lanes in a fixed order.
 // U: column steps whose loads are in flight together.
-template <typename T, int J, int U>
+template <typename T, int J, int U, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(
     const T *__restrict__ dy, const T *__restrict__ ys, const int32_t *__restrict__ position,
     const int32_t *__restrict__ kept, const float *__restrict__ weights, T *__restrict__ dys,
@@ -424,8 +439,8 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(
                         d[u] = load_vec(dy_row, c, cols);
 #pragma unroll
                         for (int j = 0; j < J; ++j)
-                            v[u][j] = load_vec(ys + (int64_t)(row[j] >= 0 ? row[j] : 0) * cols, c,
-                                               cols);
+                            v[u][j] = load_vec<STREAM>(ys + (int64_t)(row[j] >= 0 ? row[j] : 0) * cols,
+                                                       c, cols);
                     }
                 }
 #pragma unroll
@@ -444,7 +459,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(
                                 out[e] = w[j] * df[e];
                             }
                             if (row[j] >= 0)
-                                store_vec(dys + (int64_t)row[j] * cols, c, cols, narrow<T>(out));
+                                store_vec<STREAM>(dys + (int64_t)row[j] * cols, c, cols, narrow<T>(out));
                         }
                     }
                 }
@@ -479,7 +494,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(
         if (ok && e0 + g.choices > live) {
             for (int64_t e = e0 > live ? e0 : live; e < e0 + g.choices; ++e)
                 for (int c = l * V; c < g.cols; c += lanes * V)
-                    store_vec(dys + e * g.cols, c, g.cols, u32x4{});
+                    store_vec<STREAM>(dys + e * g.cols, c, g.cols, u32x4{});
         }
     }
 }
@@ -541,6 +556,15 @@ int check_rows(int64_t tokens, int32_t choices, int64_t cols, int dtype)
 }
 
 bool aligned(const void *p, int n) { return ((uintptr_t)p & (uintptr_t)(n - 1)) == 0; }
+
+// Sorted rows that the caches cannot hold: the first kernel, else the second.
+#define GSK_LAUNCH_ROWS(STREAMS, KEEPS, ...)                                                     \
+    do {                                                                                         \
+        if (tokens * choices * cols * E >= kStreamBytes)                                         \
+            hipLaunchKernelGGL(STREAMS, blocks, dim3(kRowThreads), 0, s, __VA_ARGS__);           \
+        else                                                                                     \
+            hipLaunchKernelGGL(KEEPS, blocks, dim3(kRowThreads), 0, s, __VA_ARGS__);             \
+    } while (0)
 
 // One of the kernels for 1, 2, 4 or 8 choices a round: LAUNCH(T, J).
 #define GSK_BY_CHOICES(LAUNCH, T)                                                                \
@@ -626,10 +650,11 @@ int gemm_gather_rows(const void *x, const int32_t *position, const int32_t *kept
     }
     const RowGrid g = row_grid(tokens, choices, (int32_t)cols, E);
     const dim3 blocks = row_blocks(g, E, true);
+    const hipStream_t s = (hipStream_t)stream;
     // a copy: only the element size matters
 #define GSK_GATHER(T, J)                                                                         \
-    hipLaunchKernelGGL((gather_kernel<T, J>), blocks, dim3(kRowThreads), 0, (hipStream_t)stream, \
-                       (const T *)x, position, kept, (T *)xs, g)
+    GSK_LAUNCH_ROWS((gather_kernel<T, J, true>), (gather_kernel<T, J, false>), (const T *)x,     \
+                    position, kept, (T *)xs, g)
     if (E == 4)
         GSK_BY_CHOICES(GSK_GATHER, float);
     else
@@ -657,8 +682,8 @@ int gemm_combine_rows(const void *ys, const int32_t *position, const float *weig
     const dim3 blocks = row_blocks(g, E, true);
     const hipStream_t s = (hipStream_t)stream;
 #define GSK_COMBINE(T, W, J)                                                                     \
-    hipLaunchKernelGGL((combine_kernel<T, W, J>), blocks, dim3(kRowThreads), 0, s,               \
-                       (const T *)ys, position, weights, (T *)y, g)
+    GSK_LAUNCH_ROWS((combine_kernel<T, W, J, true>), (combine_kernel<T, W, J, false>),           \
+                    (const T *)ys, position, weights, (T *)y, g)
 #define GSK_WEIGHTED(T, J) GSK_COMBINE(T, true, J)
 #define GSK_PLAIN(T, J) GSK_COMBINE(T, false, J)
 #define GSK_BY_TYPE(T)                                                                           \
@@ -703,9 +728,9 @@ int gemm_combine_rows_backward(const void *dy, const void *ys, const int32_t *po
     const dim3 blocks = row_blocks(g, E, false);
     const hipStream_t s = (hipStream_t)stream;
 #define GSK_BACK(T, J)                                                                           \
-    hipLaunchKernelGGL((combine_backward_kernel<T, J, (J > 2 ? 1 : 4 / J)>), blocks,             \
-                       dim3(kRowThreads), 0, s, (const T *)dy, (const T *)ys, position, kept,    \
-                       weights, (T *)dys, dweights, g)
+    GSK_LAUNCH_ROWS((combine_backward_kernel<T, J, (J > 2 ? 1 : 4 / J), true>),                  \
+                    (combine_backward_kernel<T, J, (J > 2 ? 1 : 4 / J), false>), (const T *)dy,  \
+                    (const T *)ys, position, kept, weights, (T *)dys, dweights, g)
     if (dtype == GEMM_F32)
         GSK_BY_CHOICES(GSK_BACK, float);
     else if (dtype == GEMM_F16)

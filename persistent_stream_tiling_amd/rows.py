@@ -27,6 +27,9 @@ import ctypes
 from dataclasses import dataclass
 
 import torch
+# the current stream's handle, without the Stream object that
+# torch.cuda.current_stream() builds around it (3.7 us of a 10 us call)
+from torch._C import _cuda_getCurrentRawStream as _current_stream
 
 from ._lib import (BF16, F16, F32, FLAG_C_INPUT_DTYPE, GROUPED_ROWS, GROUPED_ROWS_BT,
                    GROUPED_WGRAD, Adapter, Grouped, last_error, load)
@@ -85,7 +88,7 @@ def _call(dev, fn, *args):
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _call(dev, fn, *args)
-    rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    rc = fn(*args, _current_stream(dev.index))
     if rc != 0:
         kind = ValueError if rc == -1 else RuntimeError
         raise kind(f"{fn.__name__} failed ({rc}): {last_error()}")
