@@ -276,30 +276,21 @@ __global__ __launch_bounds__(64 * shrink_waves(RT, RB)) void shrink_kernel(Adapt
 }
 
 // ---------------------------------------------------------------------------
-// acc += H . B^T for the rows that have an adapter, by all waves of a workgroup
-// together: the tile's ROWS rows from m0 on; the wave's blocks of 32 x 32 start
-// at row `row0` of the tile and column col0 of C.  Of the adapters met in a
-// wave's rows, this call takes those numbered `part`, part + parts, ...
+// H in the form the matrix instruction takes.
 //
 // H is fp32 and the instruction takes 16 bits, so H is split into 16-bit terms,
 // each the rounding of what the earlier ones leave: two for fp16 (22 bits) and
 // for bf16 with bf16 results (16 bits, against the 8 of the result), three for
 // bf16 with fp32 results (24).  fp16 has not fp32's range: 16 ranks of a row
 // whose largest magnitude lies outside [2^-4, 2^15) are scaled by a power of
-// two to bring it near 2^10, and their products scaled back.  The workgroup
-// splits kChunk ranks of all its rows at a time, once, into LDS (the rings'
-// place).
-//
-// Where all rows of a 32-row block chose one adapter (prompts: long runs of
-// rows) and none is scaled, the products are added to the sums directly.
-// Otherwise a product of all the block's rows is formed in registers of its
-// own, and the rows that chose the adapter add it to theirs: so another
-// adapter's infinities and NaN never reach them.  The fp32 kernel multiplies H
-// as it is.
+// two to bring it near 2^10, and their products scaled back.  The fp32 kernel
+// multiplies H as it is.
+
 // (ranks at a time: what the registers beside the sums hold)
 constexpr int rank_chunk(int nt) { return nt == 1 ? 64 : 32; }
 
-constexpr int kTermsOf(int dt) { return dt == 2 ? 3 : 2; }  // 16-byte words of 8 ranks (fp32: as they are)
+// 16-byte words of 8 ranks (fp32: the values themselves)
+constexpr int kTermsOf(int dt) { return dt == 2 ? 3 : 2; }
 
 // LDS for ROWS rows: terms, then the scale of each row's 16 ranks.
 template <int DT, int ROWS, int NT>
@@ -321,71 +312,84 @@ __device__ __forceinline__ int term_at(int chunk, int s, int g, int h, int row)
 }
 
 template <int DT, int ROWS, int CHUNK>
-__device__ __forceinline__ void split_h(const AdapterArgs &a, uint8_t *lds, int m0, int r0, int groups)
+__device__ __forceinline__ void split_h(const AdapterArgs &a, uint8_t *lds, int m0, int r0,
+                                        int groups)
 {
     using T = typename Elem<DT>::T;
     constexpr int kTerms = kTermsOf(DT);
     u32x4 *const terms = (u32x4 *)lds;
     float *const scales = (float *)(lds + ROWS * kTerms * CHUNK * 2);
     const auto at = [](int s, int g, int h, int row) { return term_at<ROWS>(CHUNK, s, g, h, row); };
-            // four ranks per thread: neighbouring lanes hold one row's 16
-            for (int item = threadIdx.x; item < ROWS * groups * 4; item += (int)blockDim.x) {
-                const int quad = item & 3, row = (item >> 2) % ROWS, g = (item >> 2) / ROWS;
-                f32x4 h = f32x4{};
-                if (adapter_of(a, m0 + row) >= 0) {
-                    // the slices in order, eight in flight together
-                    const float *p = a.H + (int64_t)(m0 + row) * a.rank_pad + r0 + 16 * g + 4 * quad;
-                    const int64_t next = (int64_t)a.rows * a.rank_pad;
-                    for (int s0 = 0; s0 < a.slices; s0 += 8) {
-                        f32x4 v[8];
-    #pragma unroll
-                        for (int s = 0; s < 8; ++s)
-                            v[s] = *(const f32x4 *)(p + (s0 + s < a.slices ? s0 + s : s0) * next);
-    #pragma unroll
-                        for (int s = 0; s < 8; ++s)
-    #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                h[e] += s0 + s < a.slices ? v[s][e] : 0.0f;
-                    }
-                }
-                if constexpr (DT == 0) {
-                    terms[at(quad & 1, g, quad >> 1, row)] = __builtin_bit_cast(u32x4, h);
-                } else {
-                    float down = 1.0f;
-                    if constexpr (DT == 1) {
-                        float top = fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3])));
-                        top = fmaxf(top, __shfl_xor(top, 1));
-                        top = fmaxf(top, __shfl_xor(top, 2));
-                        float up = 1.0f;
-                        if (top > 0.0f && (top < 0.0625f || top >= 32768.0f) && top < __builtin_inff()) {
-                            int ex = (int)((bits_of(top) >> 23) & 255) - 137;  // top: 2^(ex + 10) * [1, 2)
-                            ex = ex < -100 ? -100 : ex;
-                            down = __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23);
-                            up = __builtin_bit_cast(float, (uint32_t)(127 + ex) << 23);
-                        }
-                        scales[g * ROWS + row] = up;  // (all four lanes the same)
-                    }
-                    float x[4];
-    #pragma unroll
+    // four ranks per thread: neighbouring lanes hold one row's 16
+    for (int item = threadIdx.x; item < ROWS * groups * 4; item += (int)blockDim.x) {
+        const int quad = item & 3, row = (item >> 2) % ROWS, g = (item >> 2) / ROWS;
+        f32x4 h = f32x4{};
+        if (adapter_of(a, m0 + row) >= 0) {
+            // the slices in order, eight in flight together
+            const float *p = a.H + (int64_t)(m0 + row) * a.rank_pad + r0 + 16 * g + 4 * quad;
+            const int64_t next = (int64_t)a.rows * a.rank_pad;
+            for (int s0 = 0; s0 < a.slices; s0 += 8) {
+                f32x4 v[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    v[s] = *(const f32x4 *)(p + (s0 + s < a.slices ? s0 + s : s0) * next);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+#pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        x[e] = h[e] * down;
-    #pragma unroll
-                    for (int s = 0; s < kTerms; ++s) {
-                        T t[4];
-    #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            t[e] = (T)x[e];
-                            // (an infinity or NaN leaves nothing for the later terms)
-                            x[e] = fabsf(x[e]) < __builtin_inff() ? x[e] - (float)t[e] : 0.0f;
-                        }
-                        u32x2 w;
-                        __builtin_memcpy(&w, t, 8);
-                        ((u32x2 *)&terms[at(s, g, quad >> 1, row)])[quad & 1] = w;
-                    }
-                }
+                        h[e] += s0 + s < a.slices ? v[s][e] : 0.0f;
             }
+        }
+        if constexpr (DT == 0) {
+            terms[at(quad & 1, g, quad >> 1, row)] = __builtin_bit_cast(u32x4, h);
+        } else {
+            float down = 1.0f;
+            if constexpr (DT == 1) {
+                float top = fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3])));
+                top = fmaxf(top, __shfl_xor(top, 1));
+                top = fmaxf(top, __shfl_xor(top, 2));
+                float up = 1.0f;
+                if (top > 0.0f && (top < 0.0625f || top >= 32768.0f) && top < __builtin_inff()) {
+                    int ex = (int)((bits_of(top) >> 23) & 255) - 137;  // top: 2^(ex + 10) * [1, 2)
+                    ex = ex < -100 ? -100 : ex;
+                    down = __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23);
+                    up = __builtin_bit_cast(float, (uint32_t)(127 + ex) << 23);
+                }
+                scales[g * ROWS + row] = up;  // (all four lanes the same)
+            }
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[e] = h[e] * down;
+#pragma unroll
+            for (int s = 0; s < kTerms; ++s) {
+                T t[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    t[e] = (T)x[e];
+                    // (an infinity or NaN leaves nothing for the later terms)
+                    x[e] = fabsf(x[e]) < __builtin_inff() ? x[e] - (float)t[e] : 0.0f;
+                }
+                u32x2 w;
+                __builtin_memcpy(&w, t, 8);
+                ((u32x2 *)&terms[at(s, g, quad >> 1, row)])[quad & 1] = w;
+            }
+        }
+    }
 }
 
+// acc += H . B^T for the rows that have an adapter, by all waves of a workgroup
+// together: the tile's ROWS rows from m0 on; the wave's blocks of 32 x 32 start
+// at row `row0` of the tile and column col0 of C.  Of the adapters met in 64 of
+// the wave's rows, this call takes those numbered `part`, part + parts, ...
+//
+// The workgroup splits kChunk ranks of all its rows at a time, once, into LDS
+// (the rings' place); the B of a few adapters is loaded together.  Where all
+// rows of a 32-row block chose one adapter (prompts: long runs of rows) and
+// none is scaled, the products are added to the sums directly.  Otherwise a
+// product of all the block's rows is formed in registers of its own, and the
+// rows that chose the adapter add it to theirs: so another adapter's infinities
+// and NaN never reach them.
 template <int DT, int ROWS, int MT, int NT>
 __device__ __forceinline__ void add_adapters(f32x16 (&acc)[MT ? MT : 1][NT], const AdapterArgs &a,
                                              uint8_t *lds, int m0, int row0, int col0, int part,

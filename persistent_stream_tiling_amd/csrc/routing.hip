@@ -321,7 +321,10 @@ __device__ __forceinline__ void load_rows(int32_t (&row)[J], const int32_t *posi
 
 // xs[position[t][j]] = x[t] for every choice j; rows past the kept ones are
 // zeroed (row e = t * choices + j by token t: rows and entries count alike).
-// J: choices per round.  Bound by the writes, choices rows for each row read.
+// J: choices per round.  Bound by the writes, choices rows for each row read:
+// 8192 tokens x 8 choices of 2048 bf16 in about 50 us, 6 TB/s.  (Walking the
+// sorted rows instead, each copying its token's row, took 72 us where this took
+// 52: it reads x eight times over.)
 template <typename T, int J, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void gather_kernel(const T *__restrict__ x,
                                                              const int32_t *__restrict__ position,
@@ -355,7 +358,8 @@ __global__ __launch_bounds__(kRowThreads) void gather_kernel(const T *__restrict
 // j, rounded once.  A dropped choice adds nothing (its loads go to row 0, so
 // that all J of a round are in flight together, and are then ignored).
 // Without weights: the plain sum, which is the gradient of gather_kernel.
-// Bound by the reads of the sorted rows.
+// Bound by the reads of the sorted rows: 8192 tokens x 8 choices of 2048 bf16 in
+// 52 us, 5.8 TB/s.
 template <typename T, bool WEIGHTS, int J, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(const T *__restrict__ ys,
                                                               const int32_t *__restrict__ position,
@@ -402,7 +406,8 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(const T *__restric
 // dw[t][j] = <dy[t], ys[position[t][j]]> (zero for a dropped choice), in one
 // pass over ys; rows of dys past the kept ones are zeroed.  The dot products
 // are summed per lane over its columns, then over the lanes in a fixed order.
-// U: column steps whose loads are in flight together.
+// U: column steps whose loads are in flight together.  4096 tokens x 2 choices
+// of 4096 fp32: 57 us, 5.8 TB/s.
 template <typename T, int J, int U, bool STREAM>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(
     const T *__restrict__ dy, const T *__restrict__ ys, const int32_t *__restrict__ position,

@@ -478,13 +478,16 @@ __device__ __forceinline__ void big_tile(const TileWork &w, uint8_t *lds, F &&f)
 
 // ---- many tiles per workgroup
 //
-// A tile of depth 2048 takes about 50 us of products, and some 13 us more were
-// spent around them by a workgroup per tile: its dispatch, finding its place,
-// the first copies' latency, the stores.  So a workgroup per CU stays and takes
-// tiles from queues, one per die, each a contiguous run of tile numbers (an
-// empty queue's workgroups help the others out); the next tile's first copies
-// are issued before this one's stores, and its number is asked for a tile
-// ahead.  Which workgroup computes a tile changes nothing in it.
+// With a workgroup per tile, a tile of depth K took 13 + K * 0.024 us (256
+// tiles of 256x256 at once, bf16): 13 us for its dispatch, finding its place,
+// the first copies' latency and the stores.  So a workgroup per CU stays and
+// takes tiles from queues, one per die, each a contiguous run of tile numbers
+// (an empty queue's workgroups help the others out); the next tile's first
+// copies are issued before this one's stores, and its number is asked for a
+// tile ahead: 9 us.  (32 groups x 2048 x 2048, depth 512: 206 -> 178 us, depth
+// 1024: 304 -> 281, depth 4096: the same within the runs' spread, at 1200
+// TFLOP/s, where power sets the clock.)  Which workgroup computes a tile
+// changes nothing in it.
 constexpr int kQueues = 8;
 
 struct TileQueues {
@@ -637,7 +640,9 @@ __device__ __forceinline__ void big_tiles(TileQueues *queues, uint8_t *lds, Tile
 // flight: a ring of whole 64-deep slabs (A: lines; B: lines or k-rows, as
 // above), all but one of them on their way while one is multiplied, and two
 // workgroups per CU.  MT = 1: 4 slabs of 20 KiB (60 KiB in flight per
-// workgroup); MT = 2: 3 of 24 KiB; MT = 4: 2 of 32 KiB.
+// workgroup); MT = 2: 3 of 24 KiB; MT = 4: 2 of 32 KiB.  (512 rows of 128
+// groups x 2048 x 1536 bf16: 139 us, 5.6 TB/s; one workgroup per CU with rings
+// of 8, 6 and 4 slabs: 153 us.)
 constexpr int kNarrow = 128;
 
 constexpr int narrow_stages(int mt) { return mt == 1 ? 4 : (mt == 2 ? 3 : 2); }
