@@ -505,7 +505,8 @@ size_t gemm_grouped_workspace_size(const gemm_grouped *problem);
  * GEMM_FLAG_C_INPUT_DTYPE (the only flag), the input dtype.  All arrays are
  * dense; dtype fp32, fp16 or bf16 with fp32 accumulation; the rank-sized
  * intermediate keeps at least 16 bits (22 for fp16, 24 for fp32 results).
- * Rows may be in any order.  An adapter's values, infinities and NaN among
+ * Rows may be in any order; rows of one adapter side by side are cheaper (4096
+ * rows, 64 adapters, rank 64: 0.16 ms in runs, 0.67 ms shuffled).  An adapter's values, infinities and NaN among
  * them, reach no row but those that name it.  rows < 2^24, K and N < 2^20,
  * 1 <= rank <= 128.  A serving call: it has no gradient. */
 typedef struct {

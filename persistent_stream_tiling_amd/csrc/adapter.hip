@@ -155,24 +155,18 @@ __device__ __forceinline__ void rank_step(f32x4 &sum, u32x4 ranks, u32x4 rows)
     }
 }
 
-template <int DT, int RT, int RB>  // RT: 16-rank blocks, RB: 16-row blocks
-__global__ __launch_bounds__(64 * shrink_waves(RT, RB)) void shrink_kernel(AdapterArgs a)
+// The rows from row0 on, by NW waves; lds: NW x 16 RB x (16 RT + 4) floats.
+template <int DT, int RT, int RB, int NW>  // RT: 16-rank blocks, RB: 16-row blocks
+__device__ __forceinline__ void shrink_rows(const AdapterArgs &a, float *lds, int row0)
 {
     using T = typename Elem<DT>::T;
     constexpr int V = 16 / (int)sizeof(T);  // elements per load; a step is 4 V deep
-    constexpr int NW = shrink_waves(RT, RB), kRows = 16 * RB;
-    constexpr int kPitch = RT * 16 + 4;
+    constexpr int kRows = 16 * RB, kPitch = RT * 16 + 4;
     constexpr int kAhead = RT == 1 ? 8 : (RT == 8 ? 2 : 4);  // steps per round
-    __shared__ __attribute__((aligned(16))) float red[NW][kRows][kPitch];
+    float(*const red)[kRows][kPitch] = (float(*)[kRows][kPitch])lds;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int r16 = lane & 15, q = lane >> 4;
-    const int row0 = (int)blockIdx.x * kRows;
-    if (a.parts > 1)
-        for (int i = (int)(blockIdx.y * gridDim.x + blockIdx.x) * 64 * NW + (int)threadIdx.x;
-             i < a.tiles_m * a.tiles_n; i += (int)(gridDim.x * gridDim.y) * 64 * NW)
-            a.counters[i] = 0;
-
     int id[RB];
     uint32_t has = 0;  // bit r: row row0 + r has an adapter
 #pragma unroll
@@ -272,6 +266,80 @@ __global__ __launch_bounds__(64 * shrink_waves(RT, RB)) void shrink_kernel(Adapt
             sum += red[w][row][r];
         // (the ranks past the last one are zero, whatever was multiplied there)
         h[(int64_t)row * a.rank_pad + r] = r < a.rank ? sum : 0.0f;
+    }
+}
+
+template <int DT, int RT, int RB>
+__global__ __launch_bounds__(64 * shrink_waves(RT, RB)) void shrink_kernel(AdapterArgs a)
+{
+    constexpr int NW = shrink_waves(RT, RB);
+    __shared__ __attribute__((aligned(16))) float lds[NW * 16 * RB * (RT * 16 + 4)];
+    if (a.parts > 1)
+        for (int i = (int)(blockIdx.y * gridDim.x + blockIdx.x) * 64 * NW + (int)threadIdx.x;
+             i < a.tiles_m * a.tiles_n; i += (int)(gridDim.x * gridDim.y) * 64 * NW)
+            a.counters[i] = 0;
+    shrink_rows<DT, RT, RB, NW>(a, lds, (int)blockIdx.x * 16 * RB);
+}
+
+// The same for many rows (fp16 / bf16), 64 at a time: prompts are long runs of
+// rows with one adapter, so a workgroup multiplies its rows by the whole A of
+// each adapter among them as a tile of few rows (tiles.h), operands through LDS
+// in whole lines.  Rows of more than kRuns adapters go the way above.  (The
+// whole call at 4096 x 4096, rows in runs, with shrink_kernel and with this one:
+// 4096 rows of rank 64 165 / 161 us, 8192 of rank 128 374 / 330, 8192 of rank 16
+// 261 / 255, 16384 of rank 64 618 / 597; 4096 rows of 64 adapters in any order
+// 690 / 672.)
+constexpr int kRuns = 6;
+
+template <int DT, int RT>
+__global__ __launch_bounds__(256, 2) void shrink_runs_kernel(AdapterArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[narrow_lds(2)];
+    static_assert(4 * 32 * (RT * 16 + 4) * 4 <= sizeof(lds), "LDS");
+    const int lane = threadIdx.x & 63, half = lane >> 5, l32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int row0 = (int)blockIdx.x * 64;
+    const Present present(adapter_of(a, row0 + lane), a.adapters);
+    if (present.count > kRuns) {
+        shrink_rows<DT, RT, 2, 4>(a, (float *)lds, row0);
+        __syncthreads();
+        shrink_rows<DT, RT, 2, 4>(a, (float *)lds, row0 + 32);
+        return;
+    }
+    const int k_lo = (int)blockIdx.y * a.slice_k;
+    float *const h = a.H + ((int64_t)blockIdx.y * a.rows + row0) * a.rank_pad;
+    for (int nth = 0; nth < present.count; ++nth) {
+        uint64_t rows;
+        const int mine = present.nth(nth, &rows);
+        TileWork w;
+        w.a = a.X + ((int64_t)row0 * a.ldx + k_lo) * 2;
+        w.b = a.A + ((int64_t)mine * a.rank * a.K + k_lo) * 2;
+        w.lda = a.ldx;
+        w.ldb = a.K;
+        w.m = a.rows - row0;
+        w.n = a.rank;
+        w.k = k_lo + a.slice_k < a.K ? a.slice_k : a.K - k_lo;
+        f32x16 acc[2][1];
+        narrow_tile<DT, LINES, 2>(acc, w, lds);
+        const float scale = a.scales ? a.scales[mine] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = 32 * i + l32;
+            if (!((rows >> row) & 1))
+                continue;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int r = wave * 32 + 8 * g + 4 * half;
+                f32x4 v;
+                // (the ranks past the last one are zero, whatever was multiplied there)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = r + e < a.rank ? acc[i][0][4 * g + e] * scale : 0.0f;
+                if (r < a.rank_pad)
+                    *(f32x4 *)(h + (int64_t)row * a.rank_pad + r) = v;
+            }
+        }
+        __syncthreads();  // the next adapter's slabs take the same place
     }
 }
 
@@ -739,7 +807,7 @@ int check(const gemm_adapter *p)
 struct AdapterPlan {
     int mt;                  // few-rows tiles of 32 mt x 128; 0: 256x256 (fp32: 128x128)
     int64_t tiles_m, tiles_n;
-    int parts, part_k, k_parts, rb, slices, slice_k, rank_pad;
+    int parts, part_k, k_parts, rb /* 16-row blocks */, slices, slice_k, rank_pad;
     int64_t ldx, ldw, w_rows, w_cols;
     bool pack_x, pack_w;
     size_t off_h, off_counters, off_partials, off_x, off_w, bytes;
@@ -781,11 +849,13 @@ AdapterPlan plan(const gemm_adapter *p)
     l.k_parts = l.parts;
     if (l.parts > 1)
         l.parts *= 2;  // the adapters over the other half
-    // the rank projection: blocks of 16 rows while they are few, and slices to
-    // a workgroup per CU, each at least 128 deep
+    // the rank projection: blocks of 16, 32 or 64 rows, and slices to one or two
+    // workgroups per CU, each at least 128 deep
     l.rb = p->rows <= 512 ? 1 : 2;
+    if (E == 2 && l.parts == 1 && p->K % 8 == 0 && p->rows >= 1024)
+        l.rb = 4;
     const int64_t blocks = cdiv(p->rows, 16 * l.rb);
-    int64_t slices = blocks ? kCus / blocks : 1;
+    int64_t slices = blocks ? (l.rb == 4 ? 2 * kCus : kCus) / blocks : 1;
     slices = slices < 1 ? 1 : (slices > 32 ? 32 : slices);
     const int64_t most = p->K / 128 > 0 ? p->K / 128 : 1;
     slices = slices < most ? slices : most;
@@ -830,6 +900,23 @@ void launch_shrink(const AdapterArgs &a, hipStream_t s)
 template <int DT>
 void launch_shrink(const AdapterArgs &a, int rb, hipStream_t s)
 {
+    if constexpr (DT != 0) {
+        // (A's lines have to be whole 16-byte words)
+        if (rb == 4 && ((uintptr_t)a.A & 15) == 0) {
+            const dim3 grid((unsigned)cdiv(a.rows, 64), (unsigned)a.slices);
+#define GSK_RUNS(RT) hipLaunchKernelGGL((shrink_runs_kernel<DT, RT>), grid, dim3(256), 0, s, a)
+            if (a.rank <= 16)
+                GSK_RUNS(1);
+            else if (a.rank <= 32)
+                GSK_RUNS(2);
+            else if (a.rank <= 64)
+                GSK_RUNS(4);
+            else
+                GSK_RUNS(8);
+#undef GSK_RUNS
+            return;
+        }
+    }
     if (rb == 1)
         launch_shrink<DT, 1>(a, s);
     else

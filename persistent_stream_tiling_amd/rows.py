@@ -37,7 +37,7 @@ from ._lib import (BF16, F16, F32, FLAG_C_INPUT_DTYPE, GROUPED_ROWS, GROUPED_ROW
 _CODES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
 
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)
 class Routing:
     """Entries (token, choice) sorted by group, as ``route_rows`` makes it:
     ``offsets`` (groups + 1; group g owns sorted rows offsets[g] ..
@@ -284,7 +284,8 @@ def grouped_matmul_wgrad(a, dc, offsets, out_dtype=None):
 def adapter_matmul(x, w, a, b, ids, scales=None, out_dtype=None):
     """y[t] = x[t] @ w + scales[i] * (x[t] @ a[i].T) @ b[i].T with i = ids[t],
     and x[t] @ w alone for an id outside [0, adapters): a shared projection
-    with each request's low-rank adapter, rows in any order.  ``w`` is K x N,
+    with each request's low-rank adapter, rows in any order (rows of one adapter side by
+    side are cheaper).  ``w`` is K x N,
     contiguous or the transposed view of a contiguous N x K linear-layer weight
     (read as it lies); ``a`` adapters x rank x K and ``b`` adapters x N x rank
     are the two small layers' weights; ``ids`` is int32, ``scales`` float32 per

@@ -100,6 +100,19 @@ def test_large_tiles(trans, dtype):
     check(T, K, N, 16, L, runs, dtype, False, trans)
 
 
+@pytest.mark.parametrize("r", [5, 16, 24, 40, 64, 100, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_many_rows_in_runs_and_in_any_order(r, dtype):
+    # prompts: runs of rows that end inside 64-row blocks, some rows without an
+    # adapter, a stretch of rows in any order (many adapters in a block); depth
+    # cut into slices, the last one shorter
+    T, K, N, L = 1091, 648, 3336, 40
+    rng = np.random.default_rng(r)
+    ids = np.repeat(rng.integers(-1, L, size=60), 30)[:T]
+    ids[500:800] = rng.integers(-1, L + 1, size=300)
+    check(T, K, N, r, L, torch.from_numpy(ids).int(), dtype, r % 2 == 0, True, seed=r)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_no_row_has_an_adapter(dtype):
     check(70, 136, 264, 16, 4, torch.full((70,), -1, dtype=torch.int32), dtype, True, True)

@@ -277,7 +277,7 @@ def test_layer_gradients_against_autograd_in_64_bits():
     # fp32 all the way: every stage is within its own 2 n u, so a few hundred u
     # of the largest sums involved
     for g, ref in zip(got, (Y, X.grad, W.grad, P.grad)):
-        scale = float(ref.abs().max()) * np.sqrt(max(T, K, N))
+        scale = float(ref.detach().abs().max()) * np.sqrt(max(T, K, N))
         within(g, f64(ref), 2 * (K + N + T) * U * scale)
 
 
