@@ -281,6 +281,29 @@ def test_layer_gradients_against_autograd_in_64_bits():
         within(g, f64(ref), 2 * (K + N + T) * U * scale)
 
 
+def test_gradients_against_differences():
+    # C is linear in a and in b: a difference of one entry is the gradient's
+    # entry, up to the fp32 rounding of the two sums
+    sizes, K, N = [9, 0, 20, 3], 24, 40
+    off = torch.from_numpy(offsets_of(sizes)).to(torch.int32).cuda()
+    a, b = normal((32, K), "f32", 1).cuda(), normal((4, K, N), "f32", 2).cuda()
+    dc = normal((32, N), "f32", 3).cuda()
+    da = gsk.grouped_matmul(dc, b.transpose(1, 2), off)
+    db = gsk.grouped_matmul_wgrad(a, dc, off)
+    loss = lambda x, y: float((gsk.grouped_matmul(x, y, off).double() * dc.double()).sum())  # noqa: E731
+    here = loss(a, b)
+    bound = 4 * K * U * float((a.abs().max() * b.abs().max() * dc.abs().max() * 32 * N * K))
+    for r, k in [(0, 0), (8, 23), (9, 5), (31, 11)]:
+        step = torch.zeros_like(a)
+        step[r, k] = 1.0
+        assert abs(loss(a + step, b) - here - float(da[r, k])) <= bound
+    for g, k, n in [(0, 0, 0), (1, 3, 4), (2, 23, 39), (3, 7, 20)]:
+        step = torch.zeros_like(b)
+        step[g, k, n] = 1.0
+        assert abs(loss(a, b + step) - here - float(db[g, k, n])) <= bound
+    assert (db[1] == 0).all()
+
+
 def test_captured_layer_replays():
     T, k, G, K, N = 96, 4, 12, 136, 72
     dev = dict(device="cuda")
