@@ -280,6 +280,54 @@ __global__ __launch_bounds__(512, 1) void wgrad_big_kernel(GroupedArgs a, TileLi
         });
 }
 
+// ---- B repacked: rows that are no whole 16-byte words, padded with zeros, of
+// the groups that have rows of A (a decoding step's are few: 18 rows of 69
+// groups x 952 x 1394 fp16 take 29 us, and took 75 with all groups repacked).
+constexpr int kPackThreads = 256;
+
+__global__ __launch_bounds__(kPackThreads) void pack_groups_kernel(
+    const uint16_t *__restrict__ src, uint16_t *__restrict__ dst, const int32_t *__restrict__ offsets,
+    int32_t groups, int32_t rows, int32_t matrix_rows, int32_t cols, int32_t ld, int32_t lanes_log2)
+{
+    const int32_t g = (int32_t)blockIdx.y;
+    int32_t lo, hi;
+    group_rows(offsets, g, groups, rows, &lo, &hi);
+    if (hi <= lo)
+        return;
+    const int lanes = 1 << lanes_log2, per = kPackThreads >> lanes_log2;
+    for (int32_t r = (int32_t)blockIdx.x * per + (int32_t)(threadIdx.x >> lanes_log2); r < matrix_rows;
+         r += (int32_t)gridDim.x * per) {
+        const uint16_t *s = src + ((int64_t)g * matrix_rows + r) * cols;
+        uint16_t *d = dst + ((int64_t)g * matrix_rows + r) * ld;
+        for (int c = (int)(threadIdx.x & (lanes - 1)) * 8; c < ld; c += lanes * 8) {
+            u32x4 v;
+            if (c + 8 <= cols) {
+                __builtin_memcpy(&v, s + c, 16);  // (from any element: unaligned access is on)
+            } else {
+                uint16_t e[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    e[k] = c + k < cols ? s[c + k] : (uint16_t)0;
+                __builtin_memcpy(&v, e, 16);
+            }
+            *(u32x4 *)(d + c) = v;
+        }
+    }
+}
+
+void launch_pack_groups(const GroupedArgs &a, const void *src, void *dst, int32_t matrix_rows,
+                        int32_t cols, hipStream_t s)
+{
+    int lanes_log2 = 0;
+    while ((8 << lanes_log2) < a.ldb && (1 << lanes_log2) < kPackThreads)
+        ++lanes_log2;
+    const int per = kPackThreads >> lanes_log2;
+    const int blocks = (matrix_rows + per - 1) / per;
+    hipLaunchKernelGGL(pack_groups_kernel, dim3(blocks < 512 ? blocks : 512, a.groups),
+                       dim3(kPackThreads), 0, s, (const uint16_t *)src, (uint16_t *)dst, a.offsets,
+                       a.groups, a.rows, matrix_rows, cols, a.ldb, lanes_log2);
+}
+
 int elem_bytes(int dtype)
 {
     return dtype == GEMM_F32 ? 4 : (dtype == GEMM_F16 || dtype == GEMM_BF16 ? 2 : 0);
@@ -452,11 +500,15 @@ int gemm_grouped_run(const gemm_grouped *p, const int32_t *offsets, const void *
     const hipStream_t s = (hipStream_t)stream;
     if (reads && (l.pack_a || l.pack_b)) {
         uint8_t *ws = (uint8_t *)workspace;
-        if (launch_pack_pair(A, ws, l.pack_a ? p->rows : 0, p->K, p->K, l.lda, B, ws + l.off_b,
-                             l.pack_b ? l.b_rows : 0, l.b_cols, l.b_cols, l.ldb, E, s)) {
+        const bool rows_b = wgrad && l.pack_b;  // B is rows like A, not matrices
+        if ((l.pack_a || rows_b) &&
+            launch_pack_pair(A, ws, l.pack_a ? p->rows : 0, p->K, p->K, l.lda, B, ws + l.off_b,
+                             rows_b ? l.b_rows : 0, l.b_cols, l.b_cols, l.ldb, E, s)) {
             set_error("pack launch failed: %s", hipGetErrorString(hipGetLastError()));
             return -3;
         }
+        if (l.pack_b && !wgrad)
+            launch_pack_groups(a, B, ws + l.off_b, (int32_t)(bt ? p->N : p->K), (int32_t)l.b_cols, s);
         if (l.pack_a)
             a.A = ws;
         if (l.pack_b)
